@@ -51,10 +51,13 @@ extern "C" {
 
 #define FSDP_API __attribute__((visibility("default")))
 
-#define FSDP_ABI_VERSION 9
+#define FSDP_ABI_VERSION 10
 #define FSDP_MAX_WORLD 128
 /* Bytes of the device scratch of fsdp_offload_step_units_noalloc (per device). */
 #define FSDP_OFFLOAD_SCRATCH_BYTES (32 << 20)
+
+/* Bytes of the device workspace of fsdp_grad_norm and fsdp_grad_norm_units. */
+#define FSDP_NORM_WORKSPACE_BYTES (32 << 10)
 
 /* Element formats.  A plain 32-bit integer rather than an enum type, so that
  * any value a caller passes is well defined; values other than these three
@@ -344,6 +347,71 @@ FSDP_API int fsdp_unit_gather_split(fsdp_dtype state_dt, int32_t n_states, int64
  * negative size. */
 FSDP_API int fsdp_units_in_launch(int32_t world, const int64_t* shard_numels, int32_t n_units,
                                   int64_t* shard_elements_out);
+
+/* ------------------------------------------------------------------------
+ * The global gradient norm and clipping, between the backward and the step.
+ * Clipping scales every gradient of a model by one factor, so that the norm
+ * over all of them is at most max_norm:
+ *   q = sum over tensors and elements of x^2 (64-bit squares and sums),
+ *   norm = sqrt(q),  coef = min(1, max_norm / (norm + 1e-6))
+ * each rounded once to its output's type.  A NaN gives a NaN norm and a NaN
+ * coefficient, an infinity (without a NaN) an infinite norm and coefficient 0.
+ * No elements: norm 0.  Sums are taken in a fixed order, without atomics: the
+ * same call on the same device gives the same bits.
+ *
+ * Outputs (device; each may be NULL, not all three): sumsq_out one double
+ * (what the ranks of a job add up), norm_out and coef_out one float each.
+ * max_norm: finite and >= 0 (looked at only with coef_out).
+ * workspace: device, FSDP_NORM_WORKSPACE_BYTES, 8-byte aligned; needs no
+ * preparation and keeps nothing.  Calls that may run at the same time, replays
+ * of two captured graphs among them, need a workspace and outputs each.
+ * ------------------------------------------------------------------------ */
+
+/* Norm over n_tensors tensors, each contiguous, numels[k] elements of dts[k]
+ * (host arrays; formats may differ; srcs[k] may be NULL where numels[k] == 0).
+ * Up to 160 tensors of one format a launch, then one launch that adds up.
+ * FSDP_E_SIZE for more launches than the workspace holds sums (4096). */
+FSDP_API int fsdp_grad_norm(const void* const* srcs, const int64_t* numels, const fsdp_dtype* dts,
+                            int32_t n_tensors, double max_norm, double* sumsq_out, float* norm_out,
+                            float* coef_out, void* workspace, void* stream);
+
+/* One unit of fsdp_grad_norm_units. */
+typedef struct fsdp_norm_unit {
+    const void* const* rank_grads;   /* host array [world] of device pointers, world*shard_numel each */
+    void* grad_shard;                /* device, shard_numel of the reduce-scatter's output format
+                                        (fsdp_reduce_scatter_local), or NULL: not kept */
+    int64_t shard_numel;
+} fsdp_norm_unit;
+
+/* Norm over rank `rank`'s shards of the averaged gradient of n_units units, in
+ * the trip that reduces them: the gradient is the one that
+ * fsdp_reduce_scatter_local and the fused step compute (its 16-bit rounding
+ * included), and is stored where grad_shard is not NULL.  The other ranks'
+ * shards are other calls, whose sumsq are added by fsdp_grad_norm_combine. */
+FSDP_API int fsdp_grad_norm_units(const fsdp_norm_unit* units, int32_t n_units, int32_t world, int32_t rank,
+                                  fsdp_dtype grad_dt, int32_t fp32_reduce, double max_norm, double* sumsq_out,
+                                  float* norm_out, float* coef_out, void* workspace, void* stream);
+
+/* Norm and coefficient of n sums of squares (device doubles, 8-byte aligned),
+ * added in their order: the ranks' sumsq as an all-gather or all-reduce left
+ * them.  No output may overlap sumsqs. */
+FSDP_API int fsdp_grad_norm_combine(const double* sumsqs, int32_t n, double max_norm, double* sumsq_out,
+                                    float* norm_out, float* coef_out, void* stream);
+
+/* Clip in place: x <- round(x * coef), an fp32 product rounded to the tensor's
+ * format, for n_tensors tensors (as in fsdp_grad_norm).  coef: device, one
+ * float.  A coefficient of exactly 1 leaves the tensors untouched.  No tensor
+ * may overlap another (a tensor appears once per call) or coef. */
+FSDP_API int fsdp_clip_grads(void* const* tensors, const int64_t* numels, const fsdp_dtype* dts,
+                             int32_t n_tensors, const float* coef, void* stream);
+
+/* fsdp_step_units_optim with the averaged gradient g (converted to fp32)
+ * replaced by g * coef, one fp32 product that is not rounded to 16 bits.
+ * coef: device, one float, read by the step's launches. */
+FSDP_API int fsdp_step_units_clipped(const fsdp_unit* units, int32_t n_units, int32_t world, int32_t rank,
+                                     fsdp_dtype grad_dt, int32_t fp32_reduce, fsdp_dtype state_dt,
+                                     fsdp_dtype compute_dt, const fsdp_optim_hp* hp, const float* coef,
+                                     void* stream);
 
 /* Per-tensor views of the full buffer.  [P3] "The FSDP Unit" (use_orig_params):
  * tensor k is full[off_k : off_k + numel_k]; the padding belongs to no view.

@@ -24,6 +24,13 @@ from .api import (  # noqa: F401
     units_in_launch,
     view_table,
 )
+from .norm import (  # noqa: F401
+    GradNorm,
+    fsdp_clip_grads,
+    fsdp_grad_norm,
+    fsdp_grad_norm_combine,
+    fsdp_grad_norm_units,
+)
 from .state import RankState  # noqa: F401
 from .offload import (  # noqa: F401
     OffloadState,
@@ -42,5 +49,6 @@ __all__ = [
     "fsdp_unflatten_views", "view_table", "RankState", "save_shard", "load_shard", "shard_info",
     "shard_path", "consolidate", "fsdp_host_adamw", "fsdp_offload_step", "fsdp_offload_step_units",
     "fsdp_offload_step_units_noalloc", "prepare_offload_step_units", "OffloadState", "unit_gather_split", "units_in_launch",
+    "GradNorm", "fsdp_grad_norm", "fsdp_grad_norm_units", "fsdp_grad_norm_combine", "fsdp_clip_grads",
     "UnitConfig", "from_fairseq", "from_bf16_mixed_precision",
 ]

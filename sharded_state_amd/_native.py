@@ -13,7 +13,8 @@ LIB_PATH = os.path.join(_HERE, "libfsdp_shard.so")
 F32, F16, BF16 = 0, 1, 2
 OK, E_INVAL, E_DTYPE, E_SIZE, E_ALIAS, E_HIP, E_IO, E_FORMAT = 0, -1, -2, -3, -4, -5, -6, -7
 MAX_WORLD = 128
-ABI_VERSION = 9
+ABI_VERSION = 10
+NORM_WORKSPACE_BYTES = 32 << 10
 OFFLOAD_SCRATCH_BYTES = 32 << 20
 OPT_ADAMW, OPT_SGD, OPT_ADAMAX, OPT_ADADELTA = 0, 1, 2, 3
 
@@ -90,6 +91,12 @@ class Unit(ctypes.Structure):
                 ("compute_shard", ctypes.c_void_p), ("shard_numel", ctypes.c_int64)]
 
 
+class NormUnit(ctypes.Structure):
+    """fsdp_norm_unit: one unit of a norm over units."""
+    _fields_ = [("rank_grads", ctypes.POINTER(ctypes.c_void_p)), ("grad_shard", ctypes.c_void_p),
+                ("shard_numel", ctypes.c_int64)]
+
+
 class OffloadUnit(ctypes.Structure):
     """fsdp_offload_unit: one unit of an offloaded step."""
     _fields_ = [("master", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
@@ -156,6 +163,19 @@ def lib():
     L.fsdp_step_units_optim.restype = ctypes.c_int
     L.fsdp_step_units_optim.argtypes = [ctypes.POINTER(Unit), i32, i32, i32, ctypes.c_int, i32, ctypes.c_int,
                                         ctypes.c_int, ctypes.POINTER(OptimHP), vp]
+    f64, i32p = ctypes.c_double, ctypes.POINTER(ctypes.c_int32)
+    L.fsdp_step_units_clipped.restype = ctypes.c_int
+    L.fsdp_step_units_clipped.argtypes = [ctypes.POINTER(Unit), i32, i32, i32, ctypes.c_int, i32, ctypes.c_int,
+                                          ctypes.c_int, ctypes.POINTER(OptimHP), vp, vp]
+    L.fsdp_grad_norm.restype = ctypes.c_int
+    L.fsdp_grad_norm.argtypes = [vpp, i64p, i32p, i32, f64, vp, vp, vp, vp, vp]
+    L.fsdp_grad_norm_units.restype = ctypes.c_int
+    L.fsdp_grad_norm_units.argtypes = [ctypes.POINTER(NormUnit), i32, i32, i32, ctypes.c_int, i32, f64, vp, vp, vp,
+                                       vp, vp]
+    L.fsdp_grad_norm_combine.restype = ctypes.c_int
+    L.fsdp_grad_norm_combine.argtypes = [vp, i32, f64, vp, vp, vp, vp]
+    L.fsdp_clip_grads.restype = ctypes.c_int
+    L.fsdp_clip_grads.argtypes = [vpp, i64p, i32p, i32, vp, vp]
     L.fsdp_unshard_gather.restype = ctypes.c_int
     L.fsdp_unshard_gather.argtypes = [vpp, i32, i64, ctypes.c_int, vp, vp]
     L.fsdp_unflatten_views.restype = ctypes.c_int

@@ -6,6 +6,7 @@ kernels of libfsdp_shard.so.  PyTorch supplies device memory and streams.
 
 Gradient, shard and full buffers are 1-D contiguous tensors on one device.
 """
+import contextlib
 import ctypes
 
 import torch
@@ -28,6 +29,12 @@ def _stream(stream, device):
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _on(stream):
+    """The torch stream whose allocations belong to a call on `stream` (the
+    current one for None), as a context."""
+    return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext()
 
 
 def _dev(t, name):
@@ -232,7 +239,7 @@ def fsdp_step_unit(master, exp_avg, exp_avg_sq, rank_grads, rank, fp32_reduce, h
     return full
 
 
-def fsdp_step_units(units, rank, fp32_reduce, hp, stream=None):
+def fsdp_step_units(units, rank, fp32_reduce, hp, stream=None, clip=None):
     """Step several units in as few launches as possible.  `units` is a list of
     dicts with keys master, exp_avg, exp_avg_sq, rank_grads, and either
     (peer_shards, full[, compute_shard]) for the fused step with all-gather or
@@ -240,10 +247,12 @@ def fsdp_step_units(units, rank, fp32_reduce, hp, stream=None):
     length of rank_grads), rank, dtypes and hp.  hp is an AdamWHP (AdamW,
     fsdp_step_units) or an OptimHP (any pointwise optimizer,
     fsdp_step_units_optim; state buffers it does not keep may be None).
+    clip: the coefficient of a GradNorm, or one float32 element on the device,
+    by which the averaged gradient is multiplied (fsdp_step_units_clipped).
     Returns the prepared call after running it once, so a training loop can
     re-issue it without marshalling again: call(step=t) takes step t, and
     call.hp holds the hyper-parameters it reads (see prepare_step_units)."""
-    call = prepare_step_units(units, rank, fp32_reduce, hp, stream)
+    call = prepare_step_units(units, rank, fp32_reduce, hp, stream, clip)
     call()
     return call
 
@@ -254,6 +263,13 @@ def _own_hp(hp):
     if isinstance(hp, (AdamWHP, OptimHP)):
         return type(hp).from_buffer_copy(hp)
     return AdamWHP(**hp)
+
+
+def _optim_hp(hp):
+    """The same hyper-parameters as an OptimHP."""
+    if isinstance(hp, OptimHP):
+        return hp
+    return OptimHP.adamw(hp.lr, (hp.beta1, hp.beta2), hp.eps, hp.weight_decay, hp.step)
 
 
 def _reissue(fn, name, args, hp, stream, device):
@@ -280,16 +296,22 @@ def _reissue(fn, name, args, hp, stream, device):
     return call
 
 
-def prepare_step_units(units, rank, fp32_reduce, hp, stream=None):
+def prepare_step_units(units, rank, fp32_reduce, hp, stream=None, clip=None):
     """Marshal a fsdp_step_units call once; the returned callable issues it
     (call(step=t) for step t, call(stream=s) on stream s; see _reissue).  The
     state dtype is the dtype of the units' master tensors: float32 (fp32
     master, m, v) or bfloat16 / float16 (16-bit parameter, m, v; the parameter
-    shard is the compute shard, so no compute_shard is given)."""
+    shard is the compute shard, so no compute_shard is given).  With clip the
+    call reads the coefficient from that device memory at every issue, and
+    call.hp is an OptimHP."""
     if not units:
         raise ValueError("units is empty")
-    optim = isinstance(hp, OptimHP)
     hp = _own_hp(hp)
+    if clip is not None:
+        from .norm import clip_coef
+        clip = clip_coef(clip)
+        hp = _optim_hp(hp)
+    optim = isinstance(hp, OptimHP)
     n_states = hp.n_states if optim else 2
     world = len(units[0]["rank_grads"])
     gather = units[0].get("full") is not None
@@ -366,10 +388,15 @@ def prepare_step_units(units, rank, fp32_reduce, hp, stream=None):
                         v.data_ptr() if v is not None else None, gptr, pptr,
                         full.data_ptr() if full is not None else None,
                         cs.data_ptr() if cs is not None else None, S)
+    if clip is not None:
+        tensors.append(clip)
     _same_device(tensors)
     args = (table, len(units), world, int(rank), dtype_code(gdt), int(bool(fp32_reduce)), dtype_code(sdt),
             dtype_code(cdt or torch.float32), ctypes.byref(hp), None)
     name = "fsdp_step_units_optim" if optim else "fsdp_step_units"
+    if clip is not None:
+        name = "fsdp_step_units_clipped"
+        args = args[:-1] + (ctypes.c_void_p(clip.data_ptr()), None)
     call = _reissue(getattr(N.lib(), name), name, args, hp, stream, device)
     call.keep = (keep, table, hp, tensors)   # the C side reads these host arrays at every call
     return call

@@ -26,6 +26,7 @@ import torch
 
 from . import _native as N
 from .api import fsdp_step_units
+from .norm import fsdp_grad_norm_units
 
 # the pages' pointwise optimizers (compatible) and their examples of others (not)
 POINTWISE = ("adam", "adamw", "adadelta", "adamax", "sgd")
@@ -119,14 +120,22 @@ class UnitConfig:
                 raise ValueError("units[%d]: with reshard after forward the second all-gather reads a persistent "
                                  "compute shard (compute_shard)" % k)
 
-    def step(self, units, hp, stream=None):
+    def step(self, units, hp, stream=None, clip=None):
         """``fsdp_step_units`` on a table checked against this configuration
         (the first all-gather of the step; with two gathers per step the
-        caller gathers again from the shards after the forward)."""
+        caller gathers again from the shards after the forward).  clip: a
+        clipping coefficient, as from ``grad_norm``."""
         if self.cpu_offload:
             raise ValueError("a CPU-offload configuration steps through OffloadState")
         self.check_units(units)
-        return fsdp_step_units(units, self.rank, self.fp32_reduce_scatter, hp, stream)
+        return fsdp_step_units(units, self.rank, self.fp32_reduce_scatter, hp, stream, clip)
+
+    def grad_norm(self, units, max_norm=None, out=None, stream=None):
+        """``fsdp_grad_norm_units`` on a table checked against this
+        configuration: the norm of this rank's shards of the averaged gradient,
+        and with max_norm the coefficient that ``step`` takes as clip."""
+        self.check_units(units)
+        return fsdp_grad_norm_units(units, self.rank, self.fp32_reduce_scatter, max_norm, out, stream)
 
 
 def from_fairseq(world, rank, *, ddp_backend="fully_sharded", fp16=False, memory_efficient_fp16=False,

@@ -11,6 +11,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <exception>
 #include <vector>
 
 #include "fsdp_internal.h"
@@ -95,34 +96,21 @@ int check_hp(const char* fn, const fsdp_adamw_hp* hp) {
     return FSDP_OK;
 }
 
-}  // namespace fsdp
-
-namespace {
-
-using fsdp::dt_size;
-using fsdp::fail;
-using fsdp::hip_fail;
-using fsdp::ok;
-using fsdp::valid_dtype;
-using fsdp::adam_scalars;
-using fsdp::check_hp;
-using fsdp::cu_count;
-using fsdp::reduce_scalars;
-
-// Byte range [lo, lo + n) of device memory.
-struct Range {
-    uintptr_t lo;
-    uint64_t n;
-};
-Range range(const void* p, int64_t elems, int64_t esize) {
-    return Range{(uintptr_t)p, (uint64_t)elems * (uint64_t)esize};
+// No two outputs overlap and no output overlaps an input (all non-empty).
+bool disjoint(std::vector<Range> outs, const std::vector<Range>& ins) {
+    outs.erase(std::remove_if(outs.begin(), outs.end(), [](const Range& r) { return r.n == 0; }), outs.end());
+    std::sort(outs.begin(), outs.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+    for (size_t i = 1; i < outs.size(); ++i)
+        if (outs[i].lo < outs[i - 1].lo + outs[i - 1].n) return false;
+    for (const Range& r : ins) {
+        if (r.n == 0) continue;
+        // the last output starting below r's end is the only one that can reach into r
+        auto it = std::lower_bound(outs.begin(), outs.end(), r.lo + r.n,
+                                   [](const Range& a, uintptr_t v) { return a.lo < v; });
+        if (it != outs.begin() && overlaps(*(it - 1), r)) return false;
+    }
+    return true;
 }
-bool overlaps(Range a, Range b) {
-    if (a.n == 0 || b.n == 0) return false;
-    return a.lo < b.lo + b.n && b.lo < a.lo + a.n;
-}
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 // Shared validation of world / rank / shard size.
 int check_world(int32_t world, int32_t rank, int64_t S) {
@@ -151,21 +139,26 @@ int grad_blocks(const void* const* rank_grads, int32_t world, int32_t rank, int6
     return FSDP_OK;
 }
 
-// No two outputs overlap and no output overlaps an input (all non-empty).
-bool disjoint(std::vector<Range> outs, const std::vector<Range>& ins) {
-    outs.erase(std::remove_if(outs.begin(), outs.end(), [](const Range& r) { return r.n == 0; }), outs.end());
-    std::sort(outs.begin(), outs.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
-    for (size_t i = 1; i < outs.size(); ++i)
-        if (outs[i].lo < outs[i - 1].lo + outs[i - 1].n) return false;
-    for (const Range& r : ins) {
-        if (r.n == 0) continue;
-        // the last output starting below r's end is the only one that can reach into r
-        auto it = std::lower_bound(outs.begin(), outs.end(), r.lo + r.n,
-                                   [](const Range& a, uintptr_t v) { return a.lo < v; });
-        if (it != outs.begin() && overlaps(*(it - 1), r)) return false;
-    }
-    return true;
-}
+}  // namespace fsdp
+
+namespace {
+
+using fsdp::dt_size;
+using fsdp::fail;
+using fsdp::hip_fail;
+using fsdp::ok;
+using fsdp::valid_dtype;
+using fsdp::adam_scalars;
+using fsdp::aligned16;
+using fsdp::check_hp;
+using fsdp::check_world;
+using fsdp::cu_count;
+using fsdp::disjoint;
+using fsdp::grad_blocks;
+using fsdp::overlaps;
+using fsdp::Range;
+using fsdp::range;
+using fsdp::reduce_scalars;
 
 // One unit of an AdamW launch: validated, with its pointer tables.
 struct UnitBuild {
@@ -299,7 +292,7 @@ int optim_params(const char* fn, const fsdp_optim_hp* hp, fsdp::OptParams& op, i
 // Launch the validated units (one grid per table of units).
 int launch_built(const char* fn, std::vector<UnitBuild>& units, int32_t world, int grad_dt,
                  int32_t fp32_reduce, int state_dt, int compute_dt, bool gather, const fsdp::OptParams& op,
-                 const std::vector<Range>& ins, const std::vector<Range>& outs, void* stream) {
+                 const float* clip, const std::vector<Range>& ins, const std::vector<Range>& outs, void* stream) {
     if (!disjoint(outs, ins)) return fail(FSDP_E_ALIAS, "%s: an output overlaps an input or another output", fn);
     std::vector<fsdp::UnitArgs> args;
     args.reserve(units.size());
@@ -319,6 +312,7 @@ int launch_built(const char* fn, std::vector<UnitBuild>& units, int32_t world, i
     L.gather = gather;
     L.rs = reduce_scalars(world);
     L.opt = op;
+    L.clip = clip;
     L.cus = cu_count();
     L.stream = stream;
     (void)hipGetLastError();
@@ -499,8 +493,8 @@ int fsdp_sharded_adamw(float* master, float* exp_avg, float* exp_avg_sq, const v
     rc = build_unit(fn, 0, master, exp_avg, exp_avg_sq, 2, FSDP_F32, rank_grads, world, rank, grad_dt, compute_dt,
                     shard_numel, compute_shard, nullptr, nullptr, false, units[0], ins, outs);
     if (rc) return rc;
-    return launch_built(fn, units, world, grad_dt, fp32_reduce, FSDP_F32, compute_dt, false, adamw_params(*hp), ins,
-                        outs, stream);
+    return launch_built(fn, units, world, grad_dt, fp32_reduce, FSDP_F32, compute_dt, false, adamw_params(*hp),
+                        nullptr, ins, outs, stream);
 }
 
 int fsdp_step_unit(float* master, float* exp_avg, float* exp_avg_sq, const void* const* rank_grads,
@@ -516,8 +510,8 @@ int fsdp_step_unit(float* master, float* exp_avg, float* exp_avg_sq, const void*
     rc = build_unit(fn, 0, master, exp_avg, exp_avg_sq, 2, FSDP_F32, rank_grads, world, rank, grad_dt, compute_dt,
                     shard_numel, compute_shard, peer_shards, full_out, true, units[0], ins, outs);
     if (rc) return rc;
-    return launch_built(fn, units, world, grad_dt, fp32_reduce, FSDP_F32, compute_dt, true, adamw_params(*hp), ins,
-                        outs, stream);
+    return launch_built(fn, units, world, grad_dt, fp32_reduce, FSDP_F32, compute_dt, true, adamw_params(*hp),
+                        nullptr, ins, outs, stream);
 }
 
 }  // extern "C"
@@ -527,7 +521,7 @@ namespace {
 // The batched unit step of fsdp_step_units / fsdp_step_units_optim (hp checked).
 int step_units_impl(const char* fn, const fsdp_unit* units, int32_t n_units, int32_t world, int32_t rank,
                     int grad_dt, int32_t fp32_reduce, int state_dt, int compute_dt, const fsdp::OptParams& op,
-                    int n_states, bool state16_ok, void* stream) {
+                    int n_states, bool state16_ok, const float* clip, void* stream) {
     if (n_units < 0) return fail(FSDP_E_INVAL, "%s: n_units = %d < 0", fn, n_units);
     if (n_units > 0 && !units) return fail(FSDP_E_INVAL, "%s: units is NULL", fn);
     if (!valid_dtype(state_dt)) return fail(FSDP_E_DTYPE, "%s: state dtype %d unsupported", fn, state_dt);
@@ -543,6 +537,7 @@ int step_units_impl(const char* fn, const fsdp_unit* units, int32_t n_units, int
     const bool gather = units[0].full_out != nullptr;
     std::vector<UnitBuild> built(n_units);
     std::vector<Range> ins, outs;
+    if (clip) ins.push_back(range(clip, 1, 4));
     for (int32_t k = 0; k < n_units; ++k) {
         const fsdp_unit& u = units[k];
         if ((u.full_out != nullptr) != gather)
@@ -555,8 +550,8 @@ int step_units_impl(const char* fn, const fsdp_unit* units, int32_t n_units, int
                         built[k], ins, outs);
         if (rc) return rc;
     }
-    return launch_built(fn, built, world, grad_dt, fp32_reduce, state_dt, compute_dt, gather, op, ins, outs,
-                        stream);
+    return launch_built(fn, built, world, grad_dt, fp32_reduce, state_dt, compute_dt, gather, op, clip, ins,
+                        outs, stream);
 }
 
 }  // namespace
@@ -570,7 +565,7 @@ int fsdp_step_units(const fsdp_unit* units, int32_t n_units, int32_t world, int3
     int rc = check_hp(fn, hp);
     if (rc) return rc;
     return step_units_impl(fn, units, n_units, world, rank, grad_dt, fp32_reduce, state_dt, compute_dt,
-                           adamw_params(*hp), 2, true, stream);
+                           adamw_params(*hp), 2, true, nullptr, stream);
 }
 
 int fsdp_step_units_optim(const fsdp_unit* units, int32_t n_units, int32_t world, int32_t rank,
@@ -582,7 +577,25 @@ int fsdp_step_units_optim(const fsdp_unit* units, int32_t n_units, int32_t world
     int rc = optim_params(fn, hp, op, n_states);
     if (rc) return rc;
     return step_units_impl(fn, units, n_units, world, rank, grad_dt, fp32_reduce, state_dt, compute_dt, op,
-                           n_states, hp->kind == FSDP_OPT_ADAMW, stream);
+                           n_states, hp->kind == FSDP_OPT_ADAMW, nullptr, stream);
+}
+
+int fsdp_step_units_clipped(const fsdp_unit* units, int32_t n_units, int32_t world, int32_t rank,
+                            fsdp_dtype grad_dt, int32_t fp32_reduce, fsdp_dtype state_dt, fsdp_dtype compute_dt,
+                            const fsdp_optim_hp* hp, const float* coef, void* stream) {
+    const char* fn = "fsdp_step_units_clipped";
+    if (!coef) return fail(FSDP_E_INVAL, "%s: coef is NULL", fn);
+    if ((uintptr_t)coef & 3) return fail(FSDP_E_INVAL, "%s: coef is not 4-byte aligned", fn);
+    fsdp::OptParams op;
+    int n_states = 0;
+    int rc = optim_params(fn, hp, op, n_states);
+    if (rc) return rc;
+    try {
+        return step_units_impl(fn, units, n_units, world, rank, grad_dt, fp32_reduce, state_dt, compute_dt, op,
+                               n_states, hp->kind == FSDP_OPT_ADAMW, coef, stream);
+    } catch (const std::exception& e) {
+        return fail(FSDP_E_SIZE, "%s: %s", fn, e.what());   // the host's tables did not fit
+    }
 }
 
 int fsdp_unshard_gather(const void* const* shards, int32_t world, int64_t shard_numel, fsdp_dtype dt,

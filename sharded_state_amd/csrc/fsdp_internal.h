@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <vector>
+
 #include "fsdp_kernels.h"
 #include "fsdp_shard.h"
 
@@ -36,5 +38,28 @@ ReduceScalars reduce_scalars(int world);
 // FSDP_E_INVAL (message prefixed with fn) unless hp is non-NULL, step >= 1,
 // both betas lie in [0, 1) and lr, weight_decay and eps are >= 0 (not NaN).
 int check_hp(const char* fn, const fsdp_adamw_hp* hp);
+
+// Byte range [lo, lo + n) of device memory.
+struct Range {
+    uintptr_t lo;
+    uint64_t n;
+};
+inline Range range(const void* p, int64_t elems, int64_t esize) {
+    return Range{(uintptr_t)p, (uint64_t)elems * (uint64_t)esize};
+}
+inline bool overlaps(Range a, Range b) {
+    if (a.n == 0 || b.n == 0) return false;
+    return a.lo < b.lo + b.n && b.lo < a.lo + a.n;
+}
+
+inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+// No two outputs overlap and no output overlaps an input (all non-empty).
+bool disjoint(std::vector<Range> outs, const std::vector<Range>& ins);
+// Shared validation of world / rank / shard size.
+int check_world(int32_t world, int32_t rank, int64_t S);
+// Rank `rank`'s block of each rank's gradient, recorded as inputs.
+int grad_blocks(const void* const* rank_grads, int32_t world, int32_t rank, int64_t S, int grad_dt,
+                std::vector<const void*>& blocks, std::vector<Range>& ins);
 
 }  // namespace fsdp

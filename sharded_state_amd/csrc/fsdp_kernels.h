@@ -145,6 +145,7 @@ struct UnitLaunch {
     bool gather;
     ReduceScalars rs;
     OptParams opt;
+    const float* clip;             // device: factor of the averaged gradient, or null
     int cus;                       // compute units of the device (grid caps)
     void* stream;
 };

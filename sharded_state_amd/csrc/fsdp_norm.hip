@@ -1,0 +1,320 @@
+// fsdp_norm.hip -- gfx950 kernels of the global gradient norm and of clipping.
+//
+//   q = sum over tensors and elements of x^2,  norm = sqrt(q),
+//   coef = min(1, max_norm / (norm + 1e-6)),   x <- round(x * coef)
+//
+// Squares and sums are held in 64 bits: a 16-bit or fp32 value is exact in a
+// double, its square neither overflows nor vanishes there (fp32 squares do
+// beyond 1.8e19 and below 1e-23), and 10^9 terms lose about 1e-13 of the sum.
+// The three operations an element that this costs (widen, convert, fma) run at
+// a quarter of what the VALU could issue while HBM delivers the elements, so
+// the sum stays an HBM stream.
+// Workgroup b adds the chunks b, b + grid, ... in that order and writes one
+// partial sum; a second launch of one workgroup adds the partial sums in their
+// order.  No atomics: the result depends on the sizes and the device alone.
+#include "fsdp_device.h"
+#include "fsdp_norm.h"
+
+#pragma clang fp contract(off)
+
+namespace fsdp {
+
+// 16 bytes at any address (global accesses need no alignment on this target;
+// an address off the 16-byte grid costs a second cache line now and then).
+typedef u32x4 u32x4_any __attribute__((aligned(1)));
+
+__device__ __forceinline__ double sq(float x, double acc) {
+    const double d = (double)x;
+    return __builtin_fma(d, d, acc);
+}
+
+// The squares of the elements of one 16-byte vector of format F.
+template <int F>
+__device__ __forceinline__ void sq16(u32x4 v, double& a, double& b) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (F == FSDP_F32) {
+            if (k & 1) b = sq(to_f32<F>(w[k]), b);
+            else a = sq(to_f32<F>(w[k]), a);
+        } else {
+            a = sq(to_f32<F>(w[k] & 0xffffu), a);
+            b = sq(to_f32<F>(w[k] >> 16), b);
+        }
+    }
+}
+
+// The sum of `x` over the workgroup, in a fixed order; thread 0 has it.
+template <int THREADS>
+__device__ __forceinline__ double block_sum(double x) {
+    __shared__ double part[THREADS / 64];
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+    const int w = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) part[w] = x;
+    __syncthreads();
+    double s = part[0];
+#pragma unroll
+    for (int k = 1; k < THREADS / 64; ++k) s += part[k];
+    return s;
+}
+
+__device__ __forceinline__ void write_norm(double q, const NormOut& o) {
+    const double n = __builtin_sqrt(q);
+    if (o.sumsq) *o.sumsq = q;
+    if (o.norm) *o.norm = (float)n;
+    if (o.coef) {
+        const double c = o.max_norm / (n + 1e-6);
+        *o.coef = (float)(c > 1.0 ? 1.0 : c);      // a NaN norm stays NaN
+    }
+}
+
+// The tensor of a table that owns chunk c.
+__device__ __forceinline__ int tensor_of(const TensorTable& T, int64_t c) {
+    int lo = 0, hi = T.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (T.chunk_begin[mid] <= c) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+template <int F, bool FINISH>
+__global__ __launch_bounds__(kThreads) void k_sumsq(TensorTable T, double* __restrict__ partial, NormOut fin) {
+    constexpr int kEs = F == FSDP_F32 ? 4 : 2;
+    constexpr int64_t kElems = kSumChunkBytes / kEs;
+    constexpr int kU = (int)(kSumChunkBytes / 16 / kThreads);
+    const int64_t chunks = T.chunk_begin[T.count];
+    double a = 0.0, b = 0.0;
+    for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const int k = tensor_of(T, c);
+        const int64_t start = (c - T.chunk_begin[k]) * kElems;
+        const int64_t n = T.n[k] - start;
+        const char* p = (const char*)T.p[k] + start * kEs;
+        if (n >= kElems) {
+            u32x4 v[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) v[u] = *(const u32x4_any*)(p + ((int64_t)u * kThreads + threadIdx.x) * 16);
+#pragma unroll
+            for (int u = 0; u < kU; ++u) sq16<F>(v[u], a, b);
+        } else {
+            const int64_t nv = n * kEs / 16;
+            for (int64_t i = threadIdx.x; i < nv; i += kThreads) sq16<F>(*(const u32x4_any*)(p + i * 16), a, b);
+            for (int64_t i = nv * (16 / kEs) + threadIdx.x; i < n; i += kThreads) a = sq(load1<F>(p, i), a);
+        }
+    }
+    const double s = block_sum<kThreads>(a + b);
+    if (threadIdx.x == 0) {
+        if constexpr (FINISH) write_norm(s, fin);
+        else partial[blockIdx.x] = s;
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void k_norm_finish(const double* __restrict__ partial, int n, NormOut o) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < n; i += kThreads) s += partial[i];
+    s = block_sum<kThreads>(s);
+    if (threadIdx.x == 0) write_norm(s, o);
+}
+
+// The sum over the averaged gradient of a table of units: the reduce-scatter's
+// fold (fsdp_device.h) with the squares added as its epilogue, and the shard
+// stored where the caller wants it.  Vectors in the group layout for an fp32
+// shard, 8 consecutive elements for a 16-bit one, as k_reduce_scatter has them.
+template <int NW, int GF, bool FP32R>
+__global__ __launch_bounds__(kThreads) void k_norm_units(NormUnits<NW> B, ReduceScalars rs,
+                                                         double* __restrict__ partial) {
+    constexpr int OF = (FP32R || GF == FSDP_F32) ? FSDP_F32 : GF;
+    constexpr bool kGroup = OF == FSDP_F32;
+    const int64_t tiles = B.tile_begin[B.count];
+    double a = 0.0, b = 0.0;
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        int lo = 0, hi = B.count - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (B.tile_begin[mid] <= t) lo = mid;
+            else hi = mid - 1;
+        }
+        const int u = lo;
+        const auto gp = [&](int q) -> const void* { return B.g[u][q]; };
+        const int64_t j = t - B.tile_begin[u];
+        const int64_t nvec = B.nvec[u];
+        const int64_t tv = (nvec + kThreads - 1) / kThreads;
+        void* out = B.out[u];
+        if (j < tv) {
+            const int64_t vi = j * kThreads + threadIdx.x;
+            if (vi < nvec) {
+                float x[8];
+                reduce8<NW, GF, FP32R, true, kGroup>(gp, B.world, vi, x);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = finish<NW, GF, FP32R>(x[k], rs);
+                if (out) store8x<OF, kGroup>(out, vi, x);
+#pragma unroll
+                for (int k = 0; k < 8; k += 2) {
+                    a = sq(x[k], a);
+                    b = sq(x[k + 1], b);
+                }
+            }
+        } else {
+            const int64_t i = nvec * 8 + (j - tv) * kThreads + threadIdx.x;
+            if (i < B.S[u]) {
+                const float x = finish<NW, GF, FP32R>(reduce1<NW, GF, FP32R>(gp, B.world, i), rs);
+                if (out) store1<OF>(out, i, x);
+                a = sq(x, a);
+            }
+        }
+    }
+    const double s = block_sum<kThreads>(a + b);
+    if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+// round(x * c).  The product is kept apart from the conversion: fused into one
+// mixed-precision fma the compiler adds +0 to it, and a product of -0 loses its
+// sign.
+template <int F>
+__device__ __forceinline__ uint32_t scaled(uint32_t bits, float c) {
+    float y = to_f32<F>(bits) * c;
+    if constexpr (F == FSDP_F16) asm("" : "+v"(y));
+    return from_f32<F>(y);
+}
+
+// Clipping in place: one 16-byte vector a lane, as the segmented copies.  A
+// coefficient of exactly 1 leaves every element as it is, so those launches
+// end after one scalar load; a NaN coefficient (a NaN norm) is applied.
+template <int F>
+__global__ __launch_bounds__(kThreads) void k_clip(TensorTable T, const float* __restrict__ coef) {
+    constexpr int kEs = F == FSDP_F32 ? 4 : 2;
+    constexpr int64_t kElems = kClipChunkBytes / kEs;
+    const float c = *coef;
+    if (c == 1.0f) return;
+    const int64_t chunks = T.chunk_begin[T.count];
+    for (int64_t b = blockIdx.x; b < chunks; b += gridDim.x) {
+        const int k = tensor_of(T, b);
+        const int64_t start = (b - T.chunk_begin[k]) * kElems;
+        int64_t n = T.n[k] - start;
+        if (n > kElems) n = kElems;
+        char* p = (char*)T.p[k] + start * kEs;
+        const int64_t nv = n * kEs / 16;
+        if (threadIdx.x < nv) {
+            const u32x4 v = *(const u32x4_any*)(p + threadIdx.x * 16);
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (F == FSDP_F32) w[j] = scaled<F>(w[j], c);
+                else w[j] = scaled<F>(w[j] & 0xffffu, c) | (scaled<F>(w[j] >> 16, c) << 16);
+            }
+            u32x4 r;
+            r.x = w[0]; r.y = w[1]; r.z = w[2]; r.w = w[3];
+            *(u32x4_any*)(p + threadIdx.x * 16) = r;
+        }
+        // fewer than one vector's elements are left
+        const int64_t i = nv * (16 / kEs) + threadIdx.x;
+        if (i < n) {
+            if constexpr (F == FSDP_F32) ((uint32_t*)p)[i] = scaled<F>(((uint32_t*)p)[i], c);
+            else ((uint16_t*)p)[i] = (uint16_t)scaled<F>(((uint16_t*)p)[i], c);
+        }
+    }
+}
+
+// ----------------------------------------------------------------- launchers
+// Workgroups of a summing launch: 8 a CU (2048 lanes, the CU's limit).
+static int sum_grid(int64_t chunks, int slots, int cus) {
+    int64_t g = (int64_t)cus * 8;
+    if (g > slots) g = slots;
+    if (g > chunks) g = chunks;
+    return g < 1 ? 1 : (int)g;
+}
+
+hipError_t launch_sumsq(const TensorTable& t, int dt, double* partial, int slots, const NormOut* fin, int cus,
+                        int* used, void* stream) {
+    const int64_t chunks = t.chunk_begin[t.count];
+    *used = 0;
+    if (chunks <= 0) return hipSuccess;
+    hipStream_t st = (hipStream_t)stream;
+    const int g = sum_grid(chunks, slots, cus);
+    const NormOut none{};
+    if (g == 1 && fin) {
+        if (dt == FSDP_F32) launch(k_sumsq<FSDP_F32, true>, dim3(1), dim3(kThreads), st, t, partial, *fin);
+        else if (dt == FSDP_F16) launch(k_sumsq<FSDP_F16, true>, dim3(1), dim3(kThreads), st, t, partial, *fin);
+        else launch(k_sumsq<FSDP_BF16, true>, dim3(1), dim3(kThreads), st, t, partial, *fin);
+        return hipGetLastError();
+    }
+    *used = g;
+    if (dt == FSDP_F32) launch(k_sumsq<FSDP_F32, false>, dim3(g), dim3(kThreads), st, t, partial, none);
+    else if (dt == FSDP_F16) launch(k_sumsq<FSDP_F16, false>, dim3(g), dim3(kThreads), st, t, partial, none);
+    else launch(k_sumsq<FSDP_BF16, false>, dim3(g), dim3(kThreads), st, t, partial, none);
+    return hipGetLastError();
+}
+
+template <int NW>
+static hipError_t norm_units_all(const NormUnitArgs* units, int n, int world, int grad_dt, int fp32_reduce,
+                                 const ReduceScalars& rs, double* partial, int slots, int cus, int* used,
+                                 void* stream) {
+    constexpr int kMax = NormUnits<NW>::kMax;
+    const int launches = (n + kMax - 1) / kMax;
+    const int per = slots / (launches > 0 ? launches : 1);
+    const bool f32r = fp32_reduce || grad_dt == FSDP_F32;
+    *used = 0;
+    for (int done = 0; done < n; done += kMax) {
+        NormUnits<NW> B{};
+        B.world = world;
+        const int c = n - done < kMax ? n - done : kMax;
+        int64_t tiles = 0;
+        for (int k = 0; k < c; ++k) {
+            const NormUnitArgs& a = units[done + k];
+            const int64_t nvec = a.nvec & ~int64_t(63);   // whole groups; the rest joins the tail
+            B.tile_begin[k] = tiles;
+            B.nvec[k] = nvec;
+            B.S[k] = a.S;
+            B.out[k] = a.out;
+            for (int q = 0; q < world; ++q) B.g[k][q] = a.grads[q];
+            tiles += (nvec + kThreads - 1) / kThreads + (a.S - 8 * nvec + kThreads - 1) / kThreads;
+        }
+        B.count = c;
+        B.tile_begin[c] = tiles;
+        if (tiles == 0) continue;
+        const dim3 g((unsigned)sum_grid(tiles, per, cus)), th(kThreads);
+        hipStream_t st = (hipStream_t)stream;
+        double* out = partial + *used;
+        if (grad_dt == FSDP_F32) launch(k_norm_units<NW, FSDP_F32, true>, g, th, st, B, rs, out);
+        else if (grad_dt == FSDP_F16 && f32r) launch(k_norm_units<NW, FSDP_F16, true>, g, th, st, B, rs, out);
+        else if (grad_dt == FSDP_F16) launch(k_norm_units<NW, FSDP_F16, false>, g, th, st, B, rs, out);
+        else if (f32r) launch(k_norm_units<NW, FSDP_BF16, true>, g, th, st, B, rs, out);
+        else launch(k_norm_units<NW, FSDP_BF16, false>, g, th, st, B, rs, out);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        *used += (int)g.x;
+    }
+    return hipSuccess;
+}
+
+hipError_t launch_norm_units(const NormUnitArgs* units, int n, int world, int grad_dt, int fp32_reduce,
+                             const ReduceScalars& rs, double* partial, int slots, int cus, int* used, void* stream) {
+    switch (world) {
+    case 1: return norm_units_all<1>(units, n, world, grad_dt, fp32_reduce, rs, partial, slots, cus, used, stream);
+    case 2: return norm_units_all<2>(units, n, world, grad_dt, fp32_reduce, rs, partial, slots, cus, used, stream);
+    case 4: return norm_units_all<4>(units, n, world, grad_dt, fp32_reduce, rs, partial, slots, cus, used, stream);
+    case 8: return norm_units_all<8>(units, n, world, grad_dt, fp32_reduce, rs, partial, slots, cus, used, stream);
+    default: return norm_units_all<0>(units, n, world, grad_dt, fp32_reduce, rs, partial, slots, cus, used, stream);
+    }
+}
+
+hipError_t launch_norm_finish(const double* partial, int n, const NormOut& out, void* stream) {
+    launch(k_norm_finish, dim3(1), dim3(kThreads), (hipStream_t)stream, partial, n, out);
+    return hipGetLastError();
+}
+
+hipError_t launch_clip(const TensorTable& t, int dt, const float* coef, void* stream) {
+    const int64_t chunks = t.chunk_begin[t.count];
+    if (chunks <= 0) return hipSuccess;
+    // a launch holds fewer than 2^32 work items; beyond 2^22 workgroups they loop
+    const dim3 g((unsigned)(chunks < (1 << 22) ? chunks : (1 << 22))), th(kThreads);
+    hipStream_t st = (hipStream_t)stream;
+    if (dt == FSDP_F32) launch(k_clip<FSDP_F32>, g, th, st, t, coef);
+    else if (dt == FSDP_F16) launch(k_clip<FSDP_F16>, g, th, st, t, coef);
+    else launch(k_clip<FSDP_BF16>, g, th, st, t, coef);
+    return hipGetLastError();
+}
+
+}  // namespace fsdp

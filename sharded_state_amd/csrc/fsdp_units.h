@@ -32,7 +32,7 @@ namespace fsdp {
 // in contiguous 1 KB spans per instruction whatever the format).
 template <class OPT, int NW, int GF, bool FP32R, int CF, bool GATHER, int SF>
 __device__ __forceinline__ void unit_vec(const UnitBatch<NW>& B, int u, int64_t vi, const ReduceScalars& rs,
-                                         const OPT& op) {
+                                         const OPT& op, float clip) {
     constexpr int kW = CF == FSDP_F32 ? 2 : 1;      // dwordx4 per 8 compute elements
     constexpr int kP = NW > 1 ? NW - 1 : 1;
     void* __restrict__ p = B.p[u];
@@ -65,7 +65,7 @@ __device__ __forceinline__ void unit_vec(const UnitBatch<NW>& B, int u, int64_t 
     reduce8<NW, GF, FP32R, true, kG>(UnitGrads<NW>{B, u}, B.world, vi, acc);
     __builtin_amdgcn_sched_barrier(0);   // keep the loads ahead of the math
 #pragma unroll
-    for (int k = 0; k < 8; ++k) op(finish<NW, GF, FP32R>(acc[k], rs), pp[k], mm[k], vv[k]);
+    for (int k = 0; k < 8; ++k) op(finish<NW, GF, FP32R>(acc[k], rs) * clip, pp[k], mm[k], vv[k]);
     if constexpr (OPT::kStorePace > 0 && NW >= 1 && NW <= 2) __builtin_amdgcn_s_sleep(OPT::kStorePace);
     store8x<SF, kG>(p, vi, pp);
     if constexpr (OPT::kStates >= 1) store8x<SF, kG>(m, vi, mm);
@@ -102,14 +102,14 @@ __device__ __forceinline__ void unit_vec(const UnitBatch<NW>& B, int u, int64_t 
 // element of a unit whose buffers are not 16-byte aligned).
 template <class OPT, int NW, int GF, bool FP32R, int CF, bool GATHER, int SF>
 __device__ __forceinline__ void unit_elem(const UnitBatch<NW>& B, int u, int64_t i, const ReduceScalars& rs,
-                                          const OPT& op) {
+                                          const OPT& op, float clip) {
     void* __restrict__ p = B.p[u];
     void* __restrict__ m = B.m[u];
     void* __restrict__ v = B.v[u];
     float pp = load1<SF>(p, i), mm = 0.0f, vv = 0.0f;
     if constexpr (OPT::kStates >= 1) mm = load1<SF>(m, i);
     if constexpr (OPT::kStates >= 2) vv = load1<SF>(v, i);
-    op(finish<NW, GF, FP32R>(reduce1<NW, GF, FP32R>(UnitGrads<NW>{B, u}, B.world, i), rs), pp, mm, vv);
+    op(finish<NW, GF, FP32R>(reduce1<NW, GF, FP32R>(UnitGrads<NW>{B, u}, B.world, i), rs) * clip, pp, mm, vv);
     store1<SF>(p, i, pp);
     if constexpr (OPT::kStates >= 1) store1<SF>(m, i, mm);
     if constexpr (OPT::kStates >= 2) store1<SF>(v, i, vv);
@@ -137,9 +137,15 @@ __device__ __forceinline__ void unit_elem(const UnitBatch<NW>& B, int u, int64_t
 // SF is the state format: FSDP_F32 for fp32 master/m/v with a separate compute
 // copy of format CF, or a 16-bit format (CF == SF) where the parameter shard is
 // itself the compute copy.
+// The averaged gradient is multiplied by the clipping coefficient in device
+// memory at `clip`, or by 1 where there is none (one scalar load a wave, one
+// product an element; a product with 1 leaves every value as it is, so the
+// step without clipping keeps its results bit for bit).
 template <class OPT, int NW, int GF, bool FP32R, int CF, bool GATHER, int SF>
-__global__ __launch_bounds__(kThreads) void k_units(UnitBatch<NW> B, ReduceScalars rs, OPT op) {
+__global__ __launch_bounds__(kThreads) void k_units(UnitBatch<NW> B, ReduceScalars rs, OPT op,
+                                                    const float* __restrict__ clip) {
     const int64_t tile = blockIdx.x;
+    const float c = clip ? *clip : 1.0f;
     int lo = 0, hi = B.count - 1;          // unit u with tile_begin[u] <= tile < tile_begin[u+1]
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -152,24 +158,24 @@ __global__ __launch_bounds__(kThreads) void k_units(UnitBatch<NW> B, ReduceScala
     const int64_t tv = (nvec + kThreads - 1) / kThreads;
     if (j < tv) {
         const int64_t vi = j * kThreads + threadIdx.x;
-        if (vi < nvec) unit_vec<OPT, NW, GF, FP32R, CF, GATHER, SF>(B, u, vi, rs, op);
+        if (vi < nvec) unit_vec<OPT, NW, GF, FP32R, CF, GATHER, SF>(B, u, vi, rs, op, c);
     } else {
         const int64_t i = nvec * 8 + (j - tv) * kThreads + threadIdx.x;
-        if (i < B.S[u]) unit_elem<OPT, NW, GF, FP32R, CF, GATHER, SF>(B, u, i, rs, op);
+        if (i < B.S[u]) unit_elem<OPT, NW, GF, FP32R, CF, GATHER, SF>(B, u, i, rs, op, c);
     }
 }
 
 // ----------------------------------------------------------------- launchers
 template <class OPT, int NW, int GF, bool FP32R, int CF, int SF>
-static hipError_t units_go(const UnitBatch<NW>& B, int64_t tiles, bool gather, const ReduceScalars& rs,
-                           const OPT& op, hipStream_t st) {
+static hipError_t units_go(const UnitBatch<NW>& B, int64_t tiles, const UnitLaunch& L, const OPT& op,
+                           hipStream_t st) {
     constexpr unsigned lds = (SF != FSDP_F32 && NW >= 1 && NW <= 2) ? kUnitLdsBytes3 : kUnitLdsBytes;
-    if (gather)
-        launch_lds(k_units<OPT, NW, GF, FP32R, CF, true, SF>, dim3((unsigned)tiles), dim3(kThreads), lds, st, B, rs,
-                   op);
+    if (L.gather)
+        launch_lds(k_units<OPT, NW, GF, FP32R, CF, true, SF>, dim3((unsigned)tiles), dim3(kThreads), lds, st, B, L.rs,
+                   op, L.clip);
     else
-        launch_lds(k_units<OPT, NW, GF, FP32R, CF, false, SF>, dim3((unsigned)tiles), dim3(kThreads), lds, st, B, rs,
-                   op);
+        launch_lds(k_units<OPT, NW, GF, FP32R, CF, false, SF>, dim3((unsigned)tiles), dim3(kThreads), lds, st, B, L.rs,
+                   op, L.clip);
     return hipGetLastError();
 }
 
@@ -178,16 +184,16 @@ static hipError_t units_cf(const UnitBatch<NW>& B, int64_t tiles, const UnitLaun
                            hipStream_t st) {
     if constexpr (OPT::kState16) {
         if (L.state_dt == FSDP_F16)
-            return units_go<OPT, NW, GF, FP32R, FSDP_F16, FSDP_F16>(B, tiles, L.gather, L.rs, op, st);
+            return units_go<OPT, NW, GF, FP32R, FSDP_F16, FSDP_F16>(B, tiles, L, op, st);
         if (L.state_dt == FSDP_BF16)
-            return units_go<OPT, NW, GF, FP32R, FSDP_BF16, FSDP_BF16>(B, tiles, L.gather, L.rs, op, st);
+            return units_go<OPT, NW, GF, FP32R, FSDP_BF16, FSDP_BF16>(B, tiles, L, op, st);
     } else if (L.state_dt != FSDP_F32) {
         return hipErrorInvalidValue;          // rejected by the host layer first
     }
     switch (L.compute_dt) {
-    case FSDP_F32: return units_go<OPT, NW, GF, FP32R, FSDP_F32, FSDP_F32>(B, tiles, L.gather, L.rs, op, st);
-    case FSDP_F16: return units_go<OPT, NW, GF, FP32R, FSDP_F16, FSDP_F32>(B, tiles, L.gather, L.rs, op, st);
-    default: return units_go<OPT, NW, GF, FP32R, FSDP_BF16, FSDP_F32>(B, tiles, L.gather, L.rs, op, st);
+    case FSDP_F32: return units_go<OPT, NW, GF, FP32R, FSDP_F32, FSDP_F32>(B, tiles, L, op, st);
+    case FSDP_F16: return units_go<OPT, NW, GF, FP32R, FSDP_F16, FSDP_F32>(B, tiles, L, op, st);
+    default: return units_go<OPT, NW, GF, FP32R, FSDP_BF16, FSDP_F32>(B, tiles, L, op, st);
     }
 }
 

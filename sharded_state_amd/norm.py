@@ -1,0 +1,198 @@
+"""The global gradient norm and clipping, between the backward and the step.
+
+Clipping keeps the norm over every gradient of a model at or under a bound by
+one factor for all of them:
+
+    q = sum of x^2 (64 bits),  norm = sqrt(q),  coef = min(1, max_norm / (norm + 1e-6))
+
+``fsdp_grad_norm`` takes a list of gradient tensors, ``fsdp_grad_norm_units`` a
+rank's units as ``fsdp_step_units`` has them (the averaged gradient of its
+shards, reduced on the way and stored where wanted).  Nothing comes back to the
+host: ``fsdp_clip_grads`` and ``fsdp_step_units(..., clip=...)`` read the
+coefficient on the device.  A job of N processes adds the ranks' ``sumsq`` (one
+all-reduce of one double) and takes the norm of the whole from
+``fsdp_grad_norm_combine``.
+
+A norm that is not finite is applied as the formula says: an infinite one gives
+coefficient 0, a NaN one gives NaN.  A loop that wants to skip such a step reads
+``norm`` before it steps.
+"""
+import ctypes
+
+import torch
+
+from . import _native as N
+from ._native import check, i64_array, ptr_array
+from .api import _dev, _grads, _on, _same_device, _stream, dtype_code
+
+_WS = N.NORM_WORKSPACE_BYTES
+
+
+class GradNorm:
+    """Where a norm call writes: one device allocation with the sum of squares,
+    the norm, the clipping coefficient and the call's workspace.
+
+    sumsq  float64, 1 element;  norm  float32, 1 element
+    coef   float32, 1 element (None if the call had no max_norm)
+
+    Calls that may run at the same time, replays of two captured graphs among
+    them, need a GradNorm each."""
+
+    def __init__(self, device="cuda"):
+        self._buf = torch.empty(16 + _WS, dtype=torch.uint8, device=device)
+        self.has_coef = False
+
+    @property
+    def device(self):
+        return self._buf.device
+
+    @property
+    def sumsq(self):
+        return self._buf[:8].view(torch.float64)
+
+    @property
+    def norm(self):
+        return self._buf[8:12].view(torch.float32)
+
+    @property
+    def coef(self):
+        return self._buf[12:16].view(torch.float32) if self.has_coef else None
+
+    def _args(self, max_norm):
+        """(max_norm, sumsq, norm, coef) of a call, and the workspace's address."""
+        p = self._buf.data_ptr()
+        self.has_coef = max_norm is not None
+        return (float(max_norm) if self.has_coef else 0.0, ctypes.c_void_p(p), ctypes.c_void_p(p + 8),
+                ctypes.c_void_p(p + 12 if self.has_coef else None)), ctypes.c_void_p(p + 16)
+
+
+def _out(out, device, stream):
+    if out is None:
+        with _on(stream):
+            return GradNorm(device)
+    if not isinstance(out, GradNorm):
+        raise TypeError("out must be a GradNorm")
+    if out.device != device:
+        raise ValueError("out is on %s, the gradients on %s" % (out.device, device))
+    return out
+
+
+def _max_norm(max_norm):
+    if max_norm is not None and not 0.0 <= float(max_norm) < float("inf"):
+        raise ValueError("max_norm must be finite and >= 0, got %r" % (max_norm,))
+
+
+def clip_coef(clip):
+    """The device coefficient of `clip`: a GradNorm with one, or a float32
+    tensor of one element."""
+    if isinstance(clip, GradNorm):
+        if not clip.has_coef:
+            raise ValueError("the norm was taken without max_norm: it has no clipping coefficient")
+        return clip.coef
+    _dev(clip, "clip")
+    if clip.dtype != torch.float32 or clip.numel() != 1:
+        raise ValueError("clip must be a GradNorm or one float32 element")
+    return clip
+
+
+def _list(tensors, name):
+    tensors = [_dev(t, "%s[%d]" % (name, i)) for i, t in enumerate(tensors)]
+    n = len(tensors)
+    return (tensors, ptr_array([t.data_ptr() for t in tensors]), i64_array([t.numel() for t in tensors]),
+            (ctypes.c_int32 * max(n, 1))(*[dtype_code(t.dtype) for t in tensors]), n)
+
+
+def fsdp_grad_norm(tensors, max_norm=None, out=None, stream=None):
+    """Norm over a list of gradient tensors (any mix of float32, float16 and
+    bfloat16, each contiguous); with max_norm the clipping coefficient too.
+    Returns the GradNorm (`out`, or a new one)."""
+    tensors, ptrs, numels, dts, n = _list(tensors, "tensors")
+    _max_norm(max_norm)
+    if not tensors and out is None:
+        raise ValueError("no tensors and no out: nothing says which device to use")
+    device = tensors[0].device if tensors else out.device
+    _same_device(tensors)
+    out = _out(out, device, stream)
+    with torch.cuda.device(device):
+        outs, ws = out._args(max_norm)
+        check("fsdp_grad_norm", N.lib().fsdp_grad_norm(ptrs, numels, dts, n, *outs, ws, _stream(stream, device)))
+    return out
+
+
+def fsdp_grad_norm_units(units, rank, fp32_reduce, max_norm=None, out=None, stream=None):
+    """Norm over rank `rank`'s shards of the averaged gradient of `units`, in the
+    pass that reduces them.  A unit is a dict as fsdp_step_units has it:
+    rank_grads, and master or shard_numel for the shard's size; with grad_shard
+    (the dtype of fsdp_reduce_scatter_local) the averaged shard is stored there.
+    All units share world, rank and dtype.  Returns the GradNorm."""
+    _max_norm(max_norm)
+    if not units:
+        raise ValueError("units is empty")
+    world = len(units[0]["rank_grads"])
+    table = (N.NormUnit * len(units))()
+    keep, tensors, gdt = [], [], None
+    for k, u in enumerate(units):
+        shard = u.get("grad_shard")
+        if shard is not None:
+            S = shard.numel()
+        elif u.get("master") is not None:
+            S = u["master"].numel()
+        elif u.get("shard_numel") is not None:
+            S = int(u["shard_numel"])
+        else:
+            raise ValueError("units[%d] needs grad_shard, master or shard_numel" % k)
+        grads, w, g_dt = _grads(u["rank_grads"], S)
+        if w != world:
+            raise ValueError("units[%d] has %d ranks, units[0] %d" % (k, w, world))
+        gdt = gdt or g_dt
+        if g_dt != gdt:
+            raise TypeError("every unit's gradients must share one dtype")
+        if shard is not None:
+            _dev(shard, "units[%d].grad_shard" % k)
+            odt = torch.float32 if (fp32_reduce or gdt == torch.float32) else gdt
+            if shard.dtype != odt:
+                raise TypeError("units[%d].grad_shard must be %s" % (k, odt))
+            tensors.append(shard)
+        tensors += grads
+        gptr = ptr_array([g.data_ptr() for g in grads])
+        keep.append(gptr)
+        table[k] = N.NormUnit(gptr, shard.data_ptr() if shard is not None else None, S)
+    _same_device(tensors)
+    device = tensors[0].device
+    out = _out(out, device, stream)
+    with torch.cuda.device(device):
+        outs, ws = out._args(max_norm)
+        check("fsdp_grad_norm_units", N.lib().fsdp_grad_norm_units(
+            table, len(units), world, int(rank), dtype_code(gdt), int(bool(fp32_reduce)), *outs, ws,
+            _stream(stream, device)))
+    return out
+
+
+def fsdp_grad_norm_combine(sumsqs, max_norm=None, out=None, stream=None):
+    """Norm (and coefficient) of the ranks' sums of squares: a float64 device
+    tensor of their `sumsq`, added in order."""
+    _dev(sumsqs, "sumsqs")
+    _max_norm(max_norm)
+    if sumsqs.dtype != torch.float64:
+        raise TypeError("sumsqs must be float64")
+    device = sumsqs.device
+    out = _out(out, device, stream)
+    with torch.cuda.device(device):
+        outs, _ = out._args(max_norm)
+        check("fsdp_grad_norm_combine", N.lib().fsdp_grad_norm_combine(
+            ctypes.c_void_p(sumsqs.data_ptr()), sumsqs.numel(), *outs, _stream(stream, device)))
+    return out
+
+
+def fsdp_clip_grads(tensors, clip, stream=None):
+    """Scale every tensor in place by the coefficient of `clip` (a GradNorm, or
+    one float32 element on the device): an fp32 product rounded to the tensor's
+    dtype.  A coefficient of exactly 1 leaves them untouched."""
+    tensors, ptrs, numels, dts, n = _list(tensors, "tensors")
+    coef = clip_coef(clip)
+    _same_device(tensors + [coef])
+    device = coef.device
+    with torch.cuda.device(device):
+        check("fsdp_clip_grads", N.lib().fsdp_clip_grads(ptrs, numels, dts, n, ctypes.c_void_p(coef.data_ptr()),
+                                                         _stream(stream, device)))
+    return tensors
