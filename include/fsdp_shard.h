@@ -413,6 +413,54 @@ FSDP_API int fsdp_step_units_clipped(const fsdp_unit* units, int32_t n_units, in
                                      fsdp_dtype compute_dt, const fsdp_optim_hp* hp, const float* coef,
                                      void* stream);
 
+/* ------------------------------------------------------------------------
+ * 4-bit microscaled blocks: the compute copy in 17/32 byte an element, its
+ * all-gather, and the product of matrices kept that way.
+ *
+ * A block is 32 consecutive elements that share a power of two 2^e, with
+ * e = floor(log2(max|x|)) - 2 held in [-127, 127]; an element is its sign and
+ * the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 to |x| / 2^e, ties to the even
+ * code, above 6 to 6.  code = sign * 8 + index into that list.  Scale byte:
+ * e + 127.  A block that holds an infinity or a NaN has the scale byte 255 and
+ * codes 0, and stands for NaN; a block of zeros has byte 0 and keeps signs.
+ *
+ * A matrix of R rows and C columns, nb = ceil(C / 32): codes are R * nb * 16
+ * bytes, two to a byte, the first in the low nibble, codes 0 behind column C;
+ * scales are R * nb bytes.  A flat shard is a matrix of one row.  Codes are
+ * 16-byte aligned (FSDP_E_INVAL otherwise).
+ * ------------------------------------------------------------------------ */
+#define FSDP_MX4_MAX_K (1 << 23)   /* longest summed axis of fsdp_mx4_matmul */
+
+/* Quantise src (rows x cols of dt, ld elements from row to row, any alignment):
+ * with codes and scales not NULL in blocks along its rows, with codes_t and
+ * scales_t not NULL in blocks along its columns, as the matrix of cols rows and
+ * `rows` columns that is its transpose (what the gradients of a product sum
+ * over); both at once read src once where they can. */
+FSDP_API int fsdp_mx4_quantize(const void* src, fsdp_dtype dt, int64_t rows, int64_t cols, int64_t ld,
+                               void* codes, void* scales, void* codes_t, void* scales_t, void* stream);
+
+/* All-gather of quantised shards, each a matrix of one row, into the full
+ * buffer of dt: full_out[q * S + i] = element i of shard q, rounded to dt. */
+FSDP_API int fsdp_mx4_gather(const void* const* codes, const void* const* scales, int32_t world,
+                             int64_t shard_numel, fsdp_dtype dt, void* full_out, void* stream);
+
+/* All-gather of quantised shards as they are, into one matrix of one row and
+ * world * shard_numel columns.  shard_numel must be a multiple of 32
+ * (FSDP_E_SIZE), so that the shards' blocks join.  A shard that sits in its
+ * slot is not copied.  A tensor [n][k] of the unit with k and its offset
+ * multiples of 32 is then the matrix at codes + offset / 2 and
+ * scales + offset / 32. */
+FSDP_API int fsdp_mx4_gather_packed(const void* const* codes, const void* const* scales, int32_t world,
+                                    int64_t shard_numel, void* full_codes, void* full_scales, void* stream);
+
+/* out[i][j] = sum over k of A[i][k] * B[j][k] for A of m rows and B of n rows,
+ * k columns each; fp32 sums, rounded once to out_dt; ldo elements from row to
+ * row of out (any alignment).  A block that stands for NaN makes the row's (or
+ * column's) results NaN.  k = 0: zeros. */
+FSDP_API int fsdp_mx4_matmul(const void* a_codes, const void* a_scales, const void* b_codes,
+                             const void* b_scales, int64_t m, int64_t n, int64_t k, fsdp_dtype out_dt,
+                             void* out, int64_t ldo, void* stream);
+
 /* Per-tensor views of the full buffer.  [P3] "The FSDP Unit" (use_orig_params):
  * tensor k is full[off_k : off_k + numel_k]; the padding belongs to no view.
  *   views_out[n_tensors]  host, receives {off_k, numel_k}

@@ -24,6 +24,16 @@ from .api import (  # noqa: F401
     units_in_launch,
     view_table,
 )
+from .mx4 import (  # noqa: F401
+    Mx4,
+    fsdp_mx4_gather,
+    fsdp_mx4_gather_packed,
+    fsdp_mx4_linear,
+    fsdp_mx4_linear_grads,
+    fsdp_mx4_matmul,
+    fsdp_mx4_quantize,
+    fsdp_mx4_views,
+)
 from .norm import (  # noqa: F401
     GradNorm,
     fsdp_clip_grads,
@@ -50,5 +60,7 @@ __all__ = [
     "shard_path", "consolidate", "fsdp_host_adamw", "fsdp_offload_step", "fsdp_offload_step_units",
     "fsdp_offload_step_units_noalloc", "prepare_offload_step_units", "OffloadState", "unit_gather_split", "units_in_launch",
     "GradNorm", "fsdp_grad_norm", "fsdp_grad_norm_units", "fsdp_grad_norm_combine", "fsdp_clip_grads",
+    "Mx4", "fsdp_mx4_quantize", "fsdp_mx4_gather", "fsdp_mx4_gather_packed", "fsdp_mx4_views", "fsdp_mx4_matmul",
+    "fsdp_mx4_linear", "fsdp_mx4_linear_grads",
     "UnitConfig", "from_fairseq", "from_bf16_mixed_precision",
 ]

@@ -176,6 +176,14 @@ def lib():
     L.fsdp_grad_norm_combine.argtypes = [vp, i32, f64, vp, vp, vp, vp]
     L.fsdp_clip_grads.restype = ctypes.c_int
     L.fsdp_clip_grads.argtypes = [vpp, i64p, i32p, i32, vp, vp]
+    L.fsdp_mx4_quantize.restype = ctypes.c_int
+    L.fsdp_mx4_quantize.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp]
+    L.fsdp_mx4_gather.restype = ctypes.c_int
+    L.fsdp_mx4_gather.argtypes = [vpp, vpp, i32, i64, i32, vp, vp]
+    L.fsdp_mx4_gather_packed.restype = ctypes.c_int
+    L.fsdp_mx4_gather_packed.argtypes = [vpp, vpp, i32, i64, vp, vp, vp]
+    L.fsdp_mx4_matmul.restype = ctypes.c_int
+    L.fsdp_mx4_matmul.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, vp, i64, vp]
     L.fsdp_unshard_gather.restype = ctypes.c_int
     L.fsdp_unshard_gather.argtypes = [vpp, i32, i64, ctypes.c_int, vp, vp]
     L.fsdp_unflatten_views.restype = ctypes.c_int

@@ -1,0 +1,44 @@
+// fsdp_mx4.h -- internal interface between the host layer of the 4-bit
+// microscaled blocks (fsdp_mx4_abi.cpp) and their kernels (fsdp_mx4.hip,
+// fsdp_mx4_matmul.hip).  Not installed.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fsdp_kernels.h"
+
+namespace fsdp {
+
+constexpr int kMx4Block = 32;                            // elements that share a scale
+inline int64_t mx4_blocks(int64_t cols) { return (cols + kMx4Block - 1) / kMx4Block; }
+
+struct Mx4Quant {
+    const void* src;               // rows x cols, ld elements from row to row
+    int dt;
+    int64_t rows, cols, ld;
+    uint8_t* codes;                // blocks along the rows, or null
+    uint8_t* scales;
+    uint8_t* codes_t;              // blocks along the columns, or null
+    uint8_t* scales_t;
+};
+hipError_t launch_mx4_quantize(const Mx4Quant& q, void* stream);
+
+struct Mx4Shards {
+    const uint8_t* codes[FSDP_MAX_WORLD];
+    const uint8_t* scales[FSDP_MAX_WORLD];
+};
+hipError_t launch_mx4_gather(const Mx4Shards& s, int world, int64_t S, int dt, void* out, void* stream);
+
+struct Mx4Product {
+    const uint8_t *a, *sa, *b, *sb;   // codes and scales of A [m][k] and B [n][k], blocks along k
+    int64_t m, n, nb;                 // nb blocks of 32 along k
+    int dt;
+    void* out;                        // [m][n], ldo elements from row to row
+    int64_t ldo;
+    int cus;
+    void* stream;
+};
+hipError_t launch_mx4_matmul(const Mx4Product& p);
+
+}  // namespace fsdp
