@@ -22,6 +22,27 @@
 
 namespace fsdp {
 
+// ----------------------------------------------------------------- clipping
+// An optimizer policy whose gradient is multiplied by a coefficient in device
+// memory (gradient clipping by the global norm).
+template <class OPT>
+struct Clipped : OPT {
+    const float* coef;
+};
+template <class OPT> constexpr bool kClips = false;
+template <class OPT> constexpr bool kClips<Clipped<OPT>> = true;
+
+template <class OPT>
+__device__ __forceinline__ float coefficient(const OPT& op) {
+    if constexpr (kClips<OPT>) return *op.coef;
+    else return 1.0f;
+}
+template <class OPT>
+__device__ __forceinline__ float clipped(float g, float c) {
+    if constexpr (kClips<OPT>) return g * c;
+    else return g;
+}
+
 // ----------------------------------------------------------------- kernels
 // One unit's step on vector vi (8 elements of a whole group in the group
 // layout, load8g; for bf16 state, 8 consecutive elements, load8):
@@ -65,7 +86,7 @@ __device__ __forceinline__ void unit_vec(const UnitBatch<NW>& B, int u, int64_t 
     reduce8<NW, GF, FP32R, true, kG>(UnitGrads<NW>{B, u}, B.world, vi, acc);
     __builtin_amdgcn_sched_barrier(0);   // keep the loads ahead of the math
 #pragma unroll
-    for (int k = 0; k < 8; ++k) op(finish<NW, GF, FP32R>(acc[k], rs) * clip, pp[k], mm[k], vv[k]);
+    for (int k = 0; k < 8; ++k) op(clipped<OPT>(finish<NW, GF, FP32R>(acc[k], rs), clip), pp[k], mm[k], vv[k]);
     if constexpr (OPT::kStorePace > 0 && NW >= 1 && NW <= 2) __builtin_amdgcn_s_sleep(OPT::kStorePace);
     store8x<SF, kG>(p, vi, pp);
     if constexpr (OPT::kStates >= 1) store8x<SF, kG>(m, vi, mm);
@@ -109,7 +130,8 @@ __device__ __forceinline__ void unit_elem(const UnitBatch<NW>& B, int u, int64_t
     float pp = load1<SF>(p, i), mm = 0.0f, vv = 0.0f;
     if constexpr (OPT::kStates >= 1) mm = load1<SF>(m, i);
     if constexpr (OPT::kStates >= 2) vv = load1<SF>(v, i);
-    op(finish<NW, GF, FP32R>(reduce1<NW, GF, FP32R>(UnitGrads<NW>{B, u}, B.world, i), rs) * clip, pp, mm, vv);
+    op(clipped<OPT>(finish<NW, GF, FP32R>(reduce1<NW, GF, FP32R>(UnitGrads<NW>{B, u}, B.world, i), rs), clip), pp, mm,
+       vv);
     store1<SF>(p, i, pp);
     if constexpr (OPT::kStates >= 1) store1<SF>(m, i, mm);
     if constexpr (OPT::kStates >= 2) store1<SF>(v, i, vv);
@@ -137,15 +159,16 @@ __device__ __forceinline__ void unit_elem(const UnitBatch<NW>& B, int u, int64_t
 // SF is the state format: FSDP_F32 for fp32 master/m/v with a separate compute
 // copy of format CF, or a 16-bit format (CF == SF) where the parameter shard is
 // itself the compute copy.
-// The averaged gradient is multiplied by the clipping coefficient in device
-// memory at `clip`, or by 1 where there is none (one scalar load a wave, one
-// product an element; a product with 1 leaves every value as it is, so the
-// step without clipping keeps its results bit for bit).
+// With a Clipped policy the averaged gradient is multiplied by the coefficient
+// in device memory (one scalar load a wave, one product an element).  One
+// kernel for both, with the factor 1 where there is none, gave the same bits
+// but cost the step without clipping: GPT-2 XL 4.141 -> 4.184 ms, 70B x96
+// 109.8 -> 110.2, with bf16 state 92.3 -> 93.7 (three repetitions in turn), so
+// the clipped step has instantiations of its own.
 template <class OPT, int NW, int GF, bool FP32R, int CF, bool GATHER, int SF>
-__global__ __launch_bounds__(kThreads) void k_units(UnitBatch<NW> B, ReduceScalars rs, OPT op,
-                                                    const float* __restrict__ clip) {
+__global__ __launch_bounds__(kThreads) void k_units(UnitBatch<NW> B, ReduceScalars rs, OPT op) {
     const int64_t tile = blockIdx.x;
-    const float c = clip ? *clip : 1.0f;
+    const float c = coefficient(op);
     int lo = 0, hi = B.count - 1;          // unit u with tile_begin[u] <= tile < tile_begin[u+1]
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -172,10 +195,10 @@ static hipError_t units_go(const UnitBatch<NW>& B, int64_t tiles, const UnitLaun
     constexpr unsigned lds = (SF != FSDP_F32 && NW >= 1 && NW <= 2) ? kUnitLdsBytes3 : kUnitLdsBytes;
     if (L.gather)
         launch_lds(k_units<OPT, NW, GF, FP32R, CF, true, SF>, dim3((unsigned)tiles), dim3(kThreads), lds, st, B, L.rs,
-                   op, L.clip);
+                   op);
     else
         launch_lds(k_units<OPT, NW, GF, FP32R, CF, false, SF>, dim3((unsigned)tiles), dim3(kThreads), lds, st, B, L.rs,
-                   op, L.clip);
+                   op);
     return hipGetLastError();
 }
 
@@ -305,6 +328,9 @@ static hipError_t units_all(const UnitArgs* units, int n, const UnitLaunch& L, c
 // Every unit of a launch with optimizer policy `op`.
 template <class OPT>
 static hipError_t launch_units_with(const UnitArgs* units, int n, const UnitLaunch& L, const OPT& op) {
+    if constexpr (!kClips<OPT>) {
+        if (L.clip) return launch_units_with(units, n, L, Clipped<OPT>{op, L.clip});
+    }
     switch (L.world) {
     case 1: return units_all<OPT, 1>(units, n, L, op);
     case 2: return units_all<OPT, 2>(units, n, L, op);
