@@ -47,6 +47,12 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8], float f, bool fi
 
 __device__ __forceinline__ uint32_t mag(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
+// The largest of four neighbouring lanes' values, in all four of them.
+__device__ __forceinline__ uint32_t max_of_four(uint32_t a) {
+    a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0xB1, 0xF, 0xF, true));   // lanes 1 0 3 2
+    return max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0x4E, 0xF, 0xF, true));  // lanes 2 3 0 1
+}
+
 // n <= 8 elements at p (any alignment), the rest zero.
 template <int F>
 __device__ __forceinline__ void load_upto8(const char* p, int64_t n, float (&x)[8]) {
@@ -89,49 +95,102 @@ __global__ __launch_bounds__(kThreads) void k_mx4_rows(const char* __restrict__ 
         uint32_t a = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) a = max(a, mag(x[k]));
-        a = max(a, (uint32_t)__shfl_xor((int)a, 1));
-        a = max(a, (uint32_t)__shfl_xor((int)a, 2));
-        const uint32_t s = scale_byte(a);
+        const uint32_t s = scale_byte(max_of_four(a));
         reinterpret_cast<uint32_t*>(codes)[b * 4 + j] = codes8(x, to_codes(s), s != 255);
         if (j == 0) scales[b] = (uint8_t)s;
     }
 }
 
-// Blocks along the columns (the rows of the transpose): a lane owns a column
-// and takes kColBlocks blocks of 32 rows; the lanes of a wave read 64
-// consecutive elements of a row.
-constexpr int kColBlocks = 4;
-template <int F>
+// Blocks along the columns (the rows of the transpose), and with ROWS along the
+// rows too, from one read: a workgroup brings kTile x kTile elements, a lane 8
+// of a row at a time.  The rows' blocks are made from registers (four lanes a
+// block); for the columns' the tile goes through LDS as it is, and a lane takes
+// two columns of 32 rows, one read a row pair.  Workgroups go to the XCDs in
+// turn; XCD x takes one run of tiles down the columns, so what neighbouring
+// tiles write to a line of the transpose (64 bytes of codes, 4 of scales each)
+// meets in one L2.
+constexpr int kTile = 128;
+template <int F, bool ROWS>
 __global__ __launch_bounds__(kThreads) void k_mx4_cols(const char* __restrict__ src, int64_t rows, int64_t cols,
-                                                       int64_t ld, int64_t nbr, uint8_t* __restrict__ codes,
-                                                       uint8_t* __restrict__ scales) {
+                                                       int64_t ld, uint32_t tiles_r, uint32_t tiles,
+                                                       uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                                                       uint8_t* __restrict__ codes_t, uint8_t* __restrict__ scales_t) {
     constexpr int kEs = F == FSDP_F32 ? 4 : 2;
-    const int64_t col_tiles = (cols + kThreads - 1) / kThreads;
-    const int64_t row_tiles = (nbr + kColBlocks - 1) / kColBlocks;
-    for (int64_t t = blockIdx.x; t < col_tiles * row_tiles; t += gridDim.x) {
-        const int64_t c = t % col_tiles * kThreads + threadIdx.x;
-        if (c >= cols) continue;
-        const int64_t b0 = t / col_tiles * kColBlocks;
-        for (int q = 0; q < kColBlocks && b0 + q < nbr; ++q) {
-            const int64_t r0 = (b0 + q) * kMx4Block;
-            const char* p = src + (r0 * ld + c) * kEs;
-            const int64_t n = rows - r0;
-            float x[4][8];
+    constexpr int kPass = kThreads / (kTile / 8);            // rows a pass
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kTile * kTile * kEs];
+    const uint32_t x = blockIdx.x & 7, per = tiles >> 3, more = tiles & 7;
+    const uint32_t t = x * per + (x < more ? x : more) + (blockIdx.x >> 3);
+    const int64_t r0 = (int64_t)(t % tiles_r) * kTile, c0 = (int64_t)(t / tiles_r) * kTile;
+    const int64_t nb = (cols + kMx4Block - 1) / kMx4Block, nbr = (rows + kMx4Block - 1) / kMx4Block;
+    const int lr = threadIdx.x / (kTile / 8), lc = threadIdx.x % (kTile / 8) * 8;
+#pragma unroll
+    for (int q = 0; q < kTile / kPass; ++q) {
+        const int64_t r = r0 + q * kPass + lr, c = c0 + lc;
+        float v[8];
+        load_upto8<F>(src + (r * ld + c) * kEs, r < rows ? cols - c : 0, v);
+        uint8_t* o = lds + ((q * kPass + lr) * kTile + lc) * kEs;
+        if constexpr (F == FSDP_F32) {
+            u32x4 a, b;
+            a.x = __float_as_uint(v[0]); a.y = __float_as_uint(v[1]);
+            a.z = __float_as_uint(v[2]); a.w = __float_as_uint(v[3]);
+            b.x = __float_as_uint(v[4]); b.y = __float_as_uint(v[5]);
+            b.z = __float_as_uint(v[6]); b.w = __float_as_uint(v[7]);
+            *reinterpret_cast<u32x4*>(o) = a;
+            *reinterpret_cast<u32x4*>(o + 16) = b;
+        } else {
+            u32x4 a;
+            a.x = from_f32<F>(v[0]) | (from_f32<F>(v[1]) << 16);
+            a.y = from_f32<F>(v[2]) | (from_f32<F>(v[3]) << 16);
+            a.z = from_f32<F>(v[4]) | (from_f32<F>(v[5]) << 16);
+            a.w = from_f32<F>(v[6]) | (from_f32<F>(v[7]) << 16);
+            *reinterpret_cast<u32x4*>(o) = a;
+        }
+        if constexpr (ROWS) {
             uint32_t a = 0;
 #pragma unroll
-            for (int k = 0; k < kMx4Block; ++k) {
-                x[k / 8][k % 8] = k < n ? load1<F>(p, (int64_t)k * ld) : 0.0f;
-                a = max(a, mag(x[k / 8][k % 8]));
+            for (int k = 0; k < 8; ++k) a = max(a, mag(v[k]));
+            const uint32_t s = scale_byte(max_of_four(a));
+            const uint32_t w = codes8(v, to_codes(s), s != 255);
+            if (r < rows && (c >> 5) < nb) {
+                const int64_t b = r * nb + (c >> 5);
+                reinterpret_cast<uint32_t*>(codes)[b * 4 + (threadIdx.x & 3)] = w;
+                if ((threadIdx.x & 3) == 0) scales[b] = (uint8_t)s;
             }
-            const uint32_t s = scale_byte(a);
-            u32x4 w;
-            w.x = codes8(x[0], to_codes(s), s != 255);
-            w.y = codes8(x[1], to_codes(s), s != 255);
-            w.z = codes8(x[2], to_codes(s), s != 255);
-            w.w = codes8(x[3], to_codes(s), s != 255);
-            reinterpret_cast<u32x4*>(codes)[c * nbr + b0 + q] = w;
-            scales[c * nbr + b0 + q] = (uint8_t)s;
         }
+    }
+    __syncthreads();
+    const int cp = threadIdx.x % (kTile / 2) * 2, rb = threadIdx.x / (kTile / 2);
+    const int64_t b = r0 / kMx4Block + rb;
+    if (b >= nbr) return;
+    float v[2][4][8];
+    uint32_t a[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < kMx4Block; ++k) {
+        const uint8_t* o = lds + ((rb * kMx4Block + k) * kTile + cp) * kEs;
+        if constexpr (F == FSDP_F32) {
+            const u32x2 w = *reinterpret_cast<const u32x2*>(o);
+            v[0][k / 8][k % 8] = __uint_as_float(w.x);
+            v[1][k / 8][k % 8] = __uint_as_float(w.y);
+        } else {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(o);
+            v[0][k / 8][k % 8] = to_f32<F>(w & 0xffffu);
+            v[1][k / 8][k % 8] = to_f32<F>(w >> 16);
+        }
+        a[0] = max(a[0], mag(v[0][k / 8][k % 8]));
+        a[1] = max(a[1], mag(v[1][k / 8][k % 8]));
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int64_t c = c0 + cp + e;
+        if (c >= cols) break;
+        const uint32_t s = scale_byte(a[e]);
+        u32x4 w;
+        w.x = codes8(v[e][0], to_codes(s), s != 255);
+        w.y = codes8(v[e][1], to_codes(s), s != 255);
+        w.z = codes8(v[e][2], to_codes(s), s != 255);
+        w.w = codes8(v[e][3], to_codes(s), s != 255);
+        reinterpret_cast<u32x4*>(codes_t)[c * nbr + b] = w;
+        scales_t[c * nbr + b] = (uint8_t)s;
     }
 }
 
@@ -193,32 +252,36 @@ static unsigned capped(int64_t want) {
 }
 
 template <int F>
-static void quantize(const Mx4Quant& q, hipStream_t st) {
+static hipError_t quantize(const Mx4Quant& q, hipStream_t st) {
     const char* src = (const char*)q.src;
-    if (q.codes) {
-        int64_t rows = q.rows, cols = q.cols;
-        if (q.ld == cols && cols % kMx4Block == 0) {      // whole blocks row after row: one long row
-            cols *= rows;
-            rows = 1;
-        }
-        const int64_t nb = mx4_blocks(cols);
-        launch(k_mx4_rows<F>, dim3(capped((rows * nb * 4 + kThreads - 1) / kThreads)), dim3(kThreads), st, src, rows,
-               cols, q.ld, nb, q.codes, q.scales);
-    }
     if (q.codes_t) {
-        const int64_t nbr = mx4_blocks(q.rows);
-        const int64_t tiles = (q.cols + kThreads - 1) / kThreads * ((nbr + kColBlocks - 1) / kColBlocks);
-        launch(k_mx4_cols<F>, dim3(capped(tiles)), dim3(kThreads), st, src, q.rows, q.cols, q.ld, nbr, q.codes_t,
-               q.scales_t);
+        const int64_t tr = (q.rows + kTile - 1) / kTile, tc = (q.cols + kTile - 1) / kTile;
+        if (tr > (1 << 24) / tc) return hipErrorInvalidValue;       // 2^38 elements
+        const dim3 g((unsigned)(tr * tc)), th(kThreads);
+        if (q.codes)
+            launch(k_mx4_cols<F, true>, g, th, st, src, q.rows, q.cols, q.ld, (uint32_t)tr, (uint32_t)(tr * tc),
+                   q.codes, q.scales, q.codes_t, q.scales_t);
+        else
+            launch(k_mx4_cols<F, false>, g, th, st, src, q.rows, q.cols, q.ld, (uint32_t)tr, (uint32_t)(tr * tc),
+                   q.codes, q.scales, q.codes_t, q.scales_t);
+        return hipGetLastError();
     }
+    int64_t rows = q.rows, cols = q.cols;
+    if (q.ld == cols && cols % kMx4Block == 0) {      // whole blocks row after row: one long row
+        cols *= rows;
+        rows = 1;
+    }
+    const int64_t nb = mx4_blocks(cols);
+    launch(k_mx4_rows<F>, dim3(capped((rows * nb * 4 + kThreads - 1) / kThreads)), dim3(kThreads), st, src, rows,
+           cols, q.ld, nb, q.codes, q.scales);
+    return hipGetLastError();
 }
 
 hipError_t launch_mx4_quantize(const Mx4Quant& q, void* stream) {
     hipStream_t st = (hipStream_t)stream;
-    if (q.dt == FSDP_F32) quantize<FSDP_F32>(q, st);
-    else if (q.dt == FSDP_F16) quantize<FSDP_F16>(q, st);
-    else quantize<FSDP_BF16>(q, st);
-    return hipGetLastError();
+    if (q.dt == FSDP_F32) return quantize<FSDP_F32>(q, st);
+    if (q.dt == FSDP_F16) return quantize<FSDP_F16>(q, st);
+    return quantize<FSDP_BF16>(q, st);
 }
 
 hipError_t launch_mx4_gather(const Mx4Shards& s, int world, int64_t S, int dt, void* out, void* stream) {
