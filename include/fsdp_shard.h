@@ -429,7 +429,8 @@ FSDP_API int fsdp_step_units_clipped(const fsdp_unit* units, int32_t n_units, in
  * scales are R * nb bytes.  A flat shard is a matrix of one row.  Codes are
  * 16-byte aligned (FSDP_E_INVAL otherwise).
  * ------------------------------------------------------------------------ */
-#define FSDP_MX4_MAX_K (1 << 23)   /* longest summed axis of fsdp_mx4_matmul */
+#define FSDP_MX4_MAX_K (1 << 23)   /* longest summed axis of a product */
+#define FSDP_MX4_FEW 32            /* most tokens of fsdp_mx4_linear_few */
 
 /* Quantise src (rows x cols of dt, ld elements from row to row, any alignment):
  * with codes and scales not NULL in blocks along its rows, with codes_t and
@@ -460,6 +461,14 @@ FSDP_API int fsdp_mx4_gather_packed(const void* const* codes, const void* const*
 FSDP_API int fsdp_mx4_matmul(const void* a_codes, const void* a_scales, const void* b_codes,
                              const void* b_scales, int64_t m, int64_t n, int64_t k, fsdp_dtype out_dt,
                              void* out, int64_t ldo, void* stream);
+
+/* y = x W^T for m <= FSDP_MX4_FEW tokens in one launch: x [m][k] of x_dt (ldx
+ * elements from row to row, any alignment) is quantised along k on the way, as
+ * fsdp_mx4_quantize does it, and multiplied by W of n rows and k columns; the
+ * result is that of the two calls up to the order of the fp32 sums. */
+FSDP_API int fsdp_mx4_linear_few(const void* x, fsdp_dtype x_dt, int64_t m, int64_t k, int64_t ldx,
+                                 const void* w_codes, const void* w_scales, int64_t n, fsdp_dtype out_dt,
+                                 void* out, int64_t ldo, void* stream);
 
 /* Per-tensor views of the full buffer.  [P3] "The FSDP Unit" (use_orig_params):
  * tensor k is full[off_k : off_k + numel_k]; the padding belongs to no view.

@@ -15,6 +15,7 @@ OK, E_INVAL, E_DTYPE, E_SIZE, E_ALIAS, E_HIP, E_IO, E_FORMAT = 0, -1, -2, -3, -4
 MAX_WORLD = 128
 ABI_VERSION = 10
 NORM_WORKSPACE_BYTES = 32 << 10
+MX4_FEW = 32
 OFFLOAD_SCRATCH_BYTES = 32 << 20
 OPT_ADAMW, OPT_SGD, OPT_ADAMAX, OPT_ADADELTA = 0, 1, 2, 3
 
@@ -182,6 +183,8 @@ def lib():
     L.fsdp_mx4_gather.argtypes = [vpp, vpp, i32, i64, i32, vp, vp]
     L.fsdp_mx4_gather_packed.restype = ctypes.c_int
     L.fsdp_mx4_gather_packed.argtypes = [vpp, vpp, i32, i64, vp, vp, vp]
+    L.fsdp_mx4_linear_few.restype = ctypes.c_int
+    L.fsdp_mx4_linear_few.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, i32, vp, i64, vp]
     L.fsdp_mx4_matmul.restype = ctypes.c_int
     L.fsdp_mx4_matmul.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, vp, i64, vp]
     L.fsdp_unshard_gather.restype = ctypes.c_int

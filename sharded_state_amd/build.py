@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfsdp_shard.so")
 SOURCES = [os.path.join(CSRC, f) for f in (
     "fsdp_kernels.hip", "fsdp_units_adamw.hip", "fsdp_units_sgd.hip", "fsdp_units_adamax.hip",
-    "fsdp_units_adadelta.hip", "fsdp_norm.hip", "fsdp_mx4.hip", "fsdp_mx4_matmul.hip",
+    "fsdp_units_adadelta.hip", "fsdp_norm.hip", "fsdp_mx4.hip", "fsdp_mx4_matmul.hip", "fsdp_mx4_few.hip",
     "fsdp_abi.cpp", "fsdp_norm_abi.cpp", "fsdp_mx4_abi.cpp", "fsdp_ckpt.cpp", "fsdp_offload.cpp")]
 OBJDIR = os.path.join(PKG, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -41,4 +41,18 @@ struct Mx4Product {
 };
 hipError_t launch_mx4_matmul(const Mx4Product& p);
 
+struct Mx4Few {
+    const void* x;                 // [m][k] of xdt, ldx elements from row to row
+    int xdt;
+    int64_t m, k, ldx;
+    const uint8_t *w, *sw;         // codes and scales of W [n][k]
+    int64_t n, nb;
+    int dt;
+    void* out;                     // [m][n], ldo elements from row to row
+    int64_t ldo;
+    int cus;
+    void* stream;
+};
+hipError_t launch_mx4_few(const Mx4Few& p);
+
 }  // namespace fsdp

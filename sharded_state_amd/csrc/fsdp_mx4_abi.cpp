@@ -152,6 +152,39 @@ int fsdp_mx4_gather_packed(const void* const* codes, const void* const* scales, 
     });
 }
 
+int fsdp_mx4_linear_few(const void* x, fsdp_dtype x_dt, int64_t m, int64_t k, int64_t ldx, const void* w_codes,
+                        const void* w_scales, int64_t n, fsdp_dtype out_dt, void* out, int64_t ldo, void* stream) {
+    const char* fn = "fsdp_mx4_linear_few";
+    return guarded(fn, [&]() -> int {
+        if (!valid_dtype(x_dt)) return fail(FSDP_E_DTYPE, "%s: dtype %d unsupported", fn, (int)x_dt);
+        if (!valid_dtype(out_dt)) return fail(FSDP_E_DTYPE, "%s: dtype %d unsupported", fn, (int)out_dt);
+        if (m > FSDP_MX4_FEW) return fail(FSDP_E_SIZE, "%s: m = %lld > %d", fn, (long long)m, FSDP_MX4_FEW);
+        int rc = check_matrix(fn, m, k);
+        if (!rc) rc = check_matrix(fn, n, k);
+        if (!rc) rc = check_matrix(fn, m, n);
+        if (rc) return rc;
+        if (k > FSDP_MX4_MAX_K) return fail(FSDP_E_SIZE, "%s: k = %lld > %d", fn, (long long)k, FSDP_MX4_MAX_K);
+        if (m == 0 || n == 0) return ok();
+        if (!out) return fail(FSDP_E_INVAL, "%s: out is NULL", fn);
+        if (m > 1 && (ldo < n || ldx < k)) return fail(FSDP_E_INVAL, "%s: ldo or ldx is smaller than a row", fn);
+        if (m > 1 && (ldo > kMaxElems / m || ldx > kMaxElems / m))
+            return fail(FSDP_E_SIZE, "%s: ldo or ldx is too large", fn);
+        if (k > 0 && (!x || !w_codes || !w_scales)) return fail(FSDP_E_INVAL, "%s: an operand is NULL", fn);
+        if (!aligned16(w_codes)) return fail(FSDP_E_INVAL, "%s: codes must be 16-byte aligned", fn);
+        const int64_t nb = mx4_blocks(k), xs = m > 1 ? ldx : k, os = m > 1 ? ldo : n;
+        const std::vector<Range> ins = {range(x, (m - 1) * xs + k, dt_size(x_dt)), range(w_codes, n * nb, 16),
+                                        range(w_scales, n * nb, 1)};
+        if (!disjoint({range(out, (m - 1) * os + n, dt_size(out_dt))}, ins))
+            return fail(FSDP_E_ALIAS, "%s: out overlaps an operand", fn);
+        const Mx4Few p{x, (int)x_dt, m, k, xs, (const uint8_t*)w_codes, (const uint8_t*)w_scales, n, nb, (int)out_dt,
+                       out, os, cu_count(), stream};
+        (void)hipGetLastError();
+        hipError_t e = launch_mx4_few(p);
+        if (e != hipSuccess) return hip_fail(e, "product launch");
+        return ok();
+    });
+}
+
 int fsdp_mx4_matmul(const void* a_codes, const void* a_scales, const void* b_codes, const void* b_scales, int64_t m,
                     int64_t n, int64_t k, fsdp_dtype out_dt, void* out, int64_t ldo, void* stream) {
     const char* fn = "fsdp_mx4_matmul";

@@ -4,16 +4,12 @@
 
 #include <type_traits>
 
-#include "fsdp_device.h"
-#include "fsdp_mx4.h"
+#include "fsdp_mx4_device.h"
 
 #pragma clang fp contract(off)
 
 namespace fsdp {
 
-typedef u32x4 u32x4_any __attribute__((aligned(1)));
-typedef u32x2 u32x2_any __attribute__((aligned(1)));
-typedef uint32_t u32_any __attribute__((aligned(1)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr int kFp4 = 4;     // the instruction's code for 4-bit elements

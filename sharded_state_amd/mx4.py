@@ -87,6 +87,14 @@ def _matrix(t, name):
     return t, rows, cols, t.stride(0) if rows > 1 else cols
 
 
+def _result(out, rows, cols):
+    """A product's output as (tensor, row stride)."""
+    if not isinstance(out, torch.Tensor) or tuple(out.shape) != (rows, cols):
+        raise ValueError("out must be a matrix of %d x %d" % (rows, cols))
+    out, _, _, ldo = _matrix(out, "out")
+    return out, ldo
+
+
 def _target(out, rows, cols, device, stream, name):
     if out is None:
         with _on(stream):
@@ -204,9 +212,7 @@ def fsdp_mx4_matmul(a, b, out=None, dtype=torch.bfloat16, stream=None):
         with _on(stream):
             out = torch.empty((a.rows, b.rows), dtype=dtype, device=device)
     res = out
-    out, rows, cols, ldo = _matrix(out, "out")
-    if res.dim() != 2 or (rows, cols) != (a.rows, b.rows):
-        raise ValueError("out must be %d x %d" % (a.rows, b.rows))
+    out, ldo = _result(out, a.rows, b.rows)
     _same_device([a.codes, b.codes, out])
     with torch.cuda.device(device):
         check("fsdp_mx4_matmul", N.lib().fsdp_mx4_matmul(
@@ -218,13 +224,28 @@ def fsdp_mx4_matmul(a, b, out=None, dtype=torch.bfloat16, stream=None):
 
 def fsdp_mx4_linear(x, w, out=None, stream=None):
     """y = x W^T for x [tokens, in] and W an Mx4 [out, in]: x is quantised along
-    its features on the way.  y has x's dtype unless `out` says otherwise."""
+    its features on the way (up to 32 tokens within the one launch).  y has x's
+    dtype unless `out` says otherwise."""
     if not isinstance(w, Mx4):
         raise TypeError("w must be an Mx4")
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != w.cols:
         raise ValueError("x must be a matrix of %d columns" % w.cols)
-    with _on(stream):
-        return fsdp_mx4_matmul(fsdp_mx4_quantize(x, stream=stream), w, out, x.dtype, stream)
+    if x.shape[0] > N.MX4_FEW:
+        with _on(stream):
+            return fsdp_mx4_matmul(fsdp_mx4_quantize(x, stream=stream), w, out, x.dtype, stream)
+    x, m, k, ldx = _matrix(x, "x")
+    device = x.device
+    if out is None:
+        with _on(stream):
+            out = torch.empty((m, w.rows), dtype=x.dtype, device=device)
+    y, ldo = _result(out, m, w.rows)
+    _same_device([x, w.codes, y])
+    with torch.cuda.device(device):
+        check("fsdp_mx4_linear_few", N.lib().fsdp_mx4_linear_few(
+            ctypes.c_void_p(x.data_ptr()), dtype_code(x.dtype), m, k, ldx, ctypes.c_void_p(w.codes.data_ptr()),
+            ctypes.c_void_p(w.scales.data_ptr()), w.rows, dtype_code(y.dtype), ctypes.c_void_p(y.data_ptr()), ldo,
+            _stream(stream, device)))
+    return out
 
 
 def fsdp_mx4_linear_grads(dy, x, wt, dx=None, dw=None, dw_dtype=None, stream=None):

@@ -286,6 +286,44 @@ def test_linear_and_its_gradients_against_the_formula(dtype, m, n, k):
     _check_product(_f64(dw), q(DY.T), q(X.T), torch.float32, "dw")
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 17, 33), (2, 100, 512), (1, 8200, 700), (3, 16400, 96),
+                                   (16, 1280, 5000), (17, 300, 1024), (31, 8192 + 5, 160), (32, 16384 + 48, 544),
+                                   (33, 200, 96), (5, 1600, 4097), (32, 65, 9000)])
+def test_linear_of_few_tokens(dtype, m, n, k):
+    """Up to 32 tokens in one launch: strided and unaligned x and y, and the same
+    values as quantisation and product one after the other."""
+    print("case", dtype, m, n, k, flush=True)
+    es = torch.empty(0, dtype=dtype).element_size()
+    w = _random_blocks(n, k, 3, 110, 120)
+    for pad, off in ((0, 0), (3, 1)):
+        hx = Guarded((m - 1) * (k + pad) + k, dtype, offset=off * es, init=_rand(((m - 1) * (k + pad) + k,), dtype, k))
+        x = torch.as_strided(hx.t, (m, k), (k + pad, 1))
+        hy = Guarded((m - 1) * (n + pad) + n, dtype, offset=off * es)
+        y = torch.as_strided(hy.t, (m, n), (n + pad, 1))
+        assert ss.fsdp_mx4_linear(x, w, y) is y
+        hy.check("y")
+        q = ss.fsdp_mx4_quantize(x)
+        _check_product(_f64(y), _mx4_values(q), _mx4_values(w), dtype, "y")
+        if pad and m > 1:
+            gap = torch.as_strided(hy.t, (m - 1, pad), (n + pad, 1), hy.t.storage_offset() + n)
+            assert (gap.contiguous().view(torch.uint8) == 0xA5).all()
+    assert ss.fsdp_mx4_linear(x, w).dtype == dtype
+    assert torch.equal(ss.fsdp_mx4_linear(x, w), ss.fsdp_mx4_linear(x, w))
+
+
+def test_linear_of_few_tokens_with_values_that_are_not_finite():
+    m, n, k = 4, 40, 300
+    x, w = _rand((m, k), torch.bfloat16, 1), _random_blocks(n, k, 2, 110, 120)
+    x[1, 299], x[2, 0] = math.nan, math.inf
+    w.scales[7, 3] = 255
+    y = ss.fsdp_mx4_linear(x, w)
+    nan = torch.zeros(m, n, dtype=torch.bool, device="cuda")
+    nan[1], nan[2], nan[:, 7] = True, True, True
+    assert torch.equal(torch.isnan(y), nan)
+    assert torch.equal(y.isnan(), ss.fsdp_mx4_matmul(ss.fsdp_mx4_quantize(x), w).isnan())
+
+
 def test_gradients_against_differences():
     """Whole numbers that blocks hold exactly in either direction: y is bilinear
     there, so moving one element from one of them to another changes

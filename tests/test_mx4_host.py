@@ -105,6 +105,23 @@ def test_matmul_refuses():
     assert call(m=0) == N.OK and call(n=0, ldo=0) == N.OK
 
 
+def test_linear_few_refuses():
+    L = N.lib()
+
+    def call(x=FAKE, xdt=N.BF16, m=4, k=96, ldx=96, w=FAKE + (1 << 30), sw=FAKE + (2 << 30), n=64, dt=N.F16,
+             out=FAKE + (3 << 30), ldo=64):
+        return L.fsdp_mx4_linear_few(vp(x), xdt, m, k, ldx, vp(w), vp(sw), n, dt, vp(out), ldo, None)
+
+    assert call(xdt=3) == N.E_DTYPE and call(dt=-1) == N.E_DTYPE
+    assert call(m=33) == N.E_SIZE and call(m=-1) == N.E_INVAL and call(k=-1) == N.E_INVAL and call(n=-1) == N.E_INVAL
+    assert call(ldx=95) == N.E_INVAL and call(ldo=63) == N.E_INVAL
+    assert call(x=0) == N.E_INVAL and call(w=0) == N.E_INVAL and call(sw=0) == N.E_INVAL and call(out=0) == N.E_INVAL
+    assert call(w=FAKE + (1 << 30) + 1) == N.E_INVAL
+    assert call(k=(1 << 23) + 1, ldx=1 << 24) == N.E_SIZE
+    assert call(out=FAKE + 700) == N.E_ALIAS and call(out=FAKE + (2 << 30) + 191) == N.E_ALIAS
+    assert call(m=0) == N.OK and call(n=0, ldo=0) == N.OK
+
+
 def test_binding_refuses():
     z = torch.zeros(4, 64)
     for f in (lambda: ss.fsdp_mx4_quantize(z), lambda: ss.fsdp_mx4_quantize(z, form="diagonal"),
