@@ -430,7 +430,8 @@ FSDP_API int fsdp_step_units_clipped(const fsdp_unit* units, int32_t n_units, in
  * 16-byte aligned (FSDP_E_INVAL otherwise).
  * ------------------------------------------------------------------------ */
 #define FSDP_MX4_MAX_K (1 << 23)   /* longest summed axis of a product */
-#define FSDP_MX4_FEW 32            /* most tokens of fsdp_mx4_linear_few */
+#define FSDP_MX4_FEW 16            /* most tokens of fsdp_mx4_linear_few */
+#define FSDP_MX4_FEW_BLOCKS 2048   /* most blocks of its x, m * ceil(k / 32) */
 
 /* Quantise src (rows x cols of dt, ld elements from row to row, any alignment):
  * with codes and scales not NULL in blocks along its rows, with codes_t and
@@ -462,7 +463,8 @@ FSDP_API int fsdp_mx4_matmul(const void* a_codes, const void* a_scales, const vo
                              const void* b_scales, int64_t m, int64_t n, int64_t k, fsdp_dtype out_dt,
                              void* out, int64_t ldo, void* stream);
 
-/* y = x W^T for m <= FSDP_MX4_FEW tokens in one launch: x [m][k] of x_dt (ldx
+/* y = x W^T for m <= FSDP_MX4_FEW tokens with m * ceil(k / 32) <=
+ * FSDP_MX4_FEW_BLOCKS (FSDP_E_SIZE otherwise) in one launch: x [m][k] of x_dt (ldx
  * elements from row to row, any alignment) is quantised along k on the way, as
  * fsdp_mx4_quantize does it, and multiplied by W of n rows and k columns; the
  * result is that of the two calls up to the order of the fp32 sums. */

@@ -15,7 +15,7 @@ OK, E_INVAL, E_DTYPE, E_SIZE, E_ALIAS, E_HIP, E_IO, E_FORMAT = 0, -1, -2, -3, -4
 MAX_WORLD = 128
 ABI_VERSION = 10
 NORM_WORKSPACE_BYTES = 32 << 10
-MX4_FEW = 32
+MX4_FEW, MX4_FEW_BLOCKS = 16, 2048
 OFFLOAD_SCRATCH_BYTES = 32 << 20
 OPT_ADAMW, OPT_SGD, OPT_ADAMAX, OPT_ADADELTA = 0, 1, 2, 3
 

@@ -41,8 +41,10 @@ struct Mx4Product {
 };
 hipError_t launch_mx4_matmul(const Mx4Product& p);
 
+// The product for a few tokens: x as it is, or in blocks (sx not null).
 struct Mx4Few {
-    const void* x;                 // [m][k] of xdt, ldx elements from row to row
+    const void* x;                 // [m][k] of xdt, ldx elements from row to row; or codes [m][nb * 16]
+    const uint8_t* sx;             // scales [m][nb], or null
     int xdt;
     int64_t m, k, ldx;
     const uint8_t *w, *sw;         // codes and scales of W [n][k]

@@ -164,6 +164,9 @@ int fsdp_mx4_linear_few(const void* x, fsdp_dtype x_dt, int64_t m, int64_t k, in
         if (!rc) rc = check_matrix(fn, m, n);
         if (rc) return rc;
         if (k > FSDP_MX4_MAX_K) return fail(FSDP_E_SIZE, "%s: k = %lld > %d", fn, (long long)k, FSDP_MX4_MAX_K);
+        if (m * mx4_blocks(k) > FSDP_MX4_FEW_BLOCKS)
+            return fail(FSDP_E_SIZE, "%s: m = %lld rows of k = %lld are more than %d blocks", fn, (long long)m,
+                        (long long)k, FSDP_MX4_FEW_BLOCKS);
         if (m == 0 || n == 0) return ok();
         if (!out) return fail(FSDP_E_INVAL, "%s: out is NULL", fn);
         if (m > 1 && (ldo < n || ldx < k)) return fail(FSDP_E_INVAL, "%s: ldo or ldx is smaller than a row", fn);
@@ -176,7 +179,7 @@ int fsdp_mx4_linear_few(const void* x, fsdp_dtype x_dt, int64_t m, int64_t k, in
                                         range(w_scales, n * nb, 1)};
         if (!disjoint({range(out, (m - 1) * os + n, dt_size(out_dt))}, ins))
             return fail(FSDP_E_ALIAS, "%s: out overlaps an operand", fn);
-        const Mx4Few p{x, (int)x_dt, m, k, xs, (const uint8_t*)w_codes, (const uint8_t*)w_scales, n, nb, (int)out_dt,
+        const Mx4Few p{x, nullptr, (int)x_dt, m, k, xs, (const uint8_t*)w_codes, (const uint8_t*)w_scales, n, nb, (int)out_dt,
                        out, os, cu_count(), stream};
         (void)hipGetLastError();
         hipError_t e = launch_mx4_few(p);

@@ -224,13 +224,14 @@ def fsdp_mx4_matmul(a, b, out=None, dtype=torch.bfloat16, stream=None):
 
 def fsdp_mx4_linear(x, w, out=None, stream=None):
     """y = x W^T for x [tokens, in] and W an Mx4 [out, in]: x is quantised along
-    its features on the way (up to 32 tokens within the one launch).  y has x's
+    its features on the way (a few tokens, up to 2048 blocks of them, within the
+    one launch).  y has x's
     dtype unless `out` says otherwise."""
     if not isinstance(w, Mx4):
         raise TypeError("w must be an Mx4")
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != w.cols:
         raise ValueError("x must be a matrix of %d columns" % w.cols)
-    if x.shape[0] > N.MX4_FEW:
+    if x.shape[0] > N.MX4_FEW or x.shape[0] * w.scales.shape[1] > N.MX4_FEW_BLOCKS:
         with _on(stream):
             return fsdp_mx4_matmul(fsdp_mx4_quantize(x, stream=stream), w, out, x.dtype, stream)
     x, m, k, ldx = _matrix(x, "x")

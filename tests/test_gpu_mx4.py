@@ -291,8 +291,8 @@ def test_linear_and_its_gradients_against_the_formula(dtype, m, n, k):
                                    (16, 1280, 5000), (17, 300, 1024), (31, 8192 + 5, 160), (32, 16384 + 48, 544),
                                    (33, 200, 96), (5, 1600, 4097), (32, 65, 9000)])
 def test_linear_of_few_tokens(dtype, m, n, k):
-    """Up to 32 tokens in one launch: strided and unaligned x and y, and the same
-    values as quantisation and product one after the other."""
+    """Few tokens in one launch, and more: strided and unaligned x and y, and the
+    same values as quantisation and product one after the other."""
     print("case", dtype, m, n, k, flush=True)
     es = torch.empty(0, dtype=dtype).element_size()
     w = _random_blocks(n, k, 3, 110, 120)

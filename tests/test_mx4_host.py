@@ -113,11 +113,12 @@ def test_linear_few_refuses():
         return L.fsdp_mx4_linear_few(vp(x), xdt, m, k, ldx, vp(w), vp(sw), n, dt, vp(out), ldo, None)
 
     assert call(xdt=3) == N.E_DTYPE and call(dt=-1) == N.E_DTYPE
-    assert call(m=33) == N.E_SIZE and call(m=-1) == N.E_INVAL and call(k=-1) == N.E_INVAL and call(n=-1) == N.E_INVAL
+    assert call(m=17) == N.E_SIZE and call(m=-1) == N.E_INVAL and call(k=-1) == N.E_INVAL and call(n=-1) == N.E_INVAL
     assert call(ldx=95) == N.E_INVAL and call(ldo=63) == N.E_INVAL
     assert call(x=0) == N.E_INVAL and call(w=0) == N.E_INVAL and call(sw=0) == N.E_INVAL and call(out=0) == N.E_INVAL
     assert call(w=FAKE + (1 << 30) + 1) == N.E_INVAL
     assert call(k=(1 << 23) + 1, ldx=1 << 24) == N.E_SIZE
+    assert call(m=16, k=129 * 32, ldx=129 * 32) == N.E_SIZE              # 2064 blocks of x
     assert call(out=FAKE + 700) == N.E_ALIAS and call(out=FAKE + (2 << 30) + 191) == N.E_ALIAS
     assert call(m=0) == N.OK and call(n=0, ldo=0) == N.OK
 
