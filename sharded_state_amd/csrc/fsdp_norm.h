@@ -26,27 +26,30 @@ static_assert(sizeof(TensorTable) <= 4000, "tables travel in kernel arguments");
 
 // Units of one launch whose averaged gradient is summed (and stored where out
 // is not null), in tiles: nvec vectors of 8 elements, then single elements.
+// The units' gradient pointers lie one after the other, world of them each.
 template <int NW>
 struct NormUnits {
-    static constexpr int kMax = NW == 0 ? 1 : (NW <= 2 ? 70 : (NW <= 4 ? 54 : 38));
-    static constexpr int kG = NW > 0 ? NW : FSDP_MAX_WORLD;
+    static constexpr int kMax = NW == 0 ? 40 : (NW <= 2 ? 70 : (NW <= 4 ? 54 : 38));
+    static constexpr int kPtrs = NW > 0 ? NW * kMax : 280;
     int32_t count;
     int32_t world;
     int64_t tile_begin[kMax + 1];
     int64_t nvec[kMax];
     int64_t S[kMax];
     void* out[kMax];
-    const void* g[kMax][kG];
+    const void* g[kPtrs];
+    bool wide[kMax];               // every buffer starts on the 16-byte grid
 };
 static_assert(sizeof(NormUnits<1>) <= 4000 && sizeof(NormUnits<2>) <= 4000 && sizeof(NormUnits<4>) <= 4000 &&
                   sizeof(NormUnits<8>) <= 4000 && sizeof(NormUnits<0>) <= 4000,
               "tables travel in kernel arguments");
+static_assert(NormUnits<0>::kPtrs >= FSDP_MAX_WORLD, "a unit of any world fits");
 
 struct NormUnitArgs {
     const void* const* grads;      // world pointers, already offset to block `rank`
     void* out;                     // averaged shard, or null
     int64_t S;
-    int64_t nvec;                  // 8-element vectors on the wide path (0: every element scalar)
+    bool wide;
 };
 
 // Where a norm goes: sums of squares, their root and the clipping coefficient
@@ -65,17 +68,19 @@ constexpr int64_t kClipChunkBytes = 4096;
 
 inline int norm_units_max(int world) {
     return world == 1 || world == 2 ? NormUnits<2>::kMax : world == 4 ? NormUnits<4>::kMax
-         : world == 8 ? NormUnits<8>::kMax : NormUnits<0>::kMax;
+         : world == 8 ? NormUnits<8>::kMax
+         : NormUnits<0>::kPtrs / world < NormUnits<0>::kMax ? NormUnits<0>::kPtrs / world : NormUnits<0>::kMax;
 }
 
 // Sums of squares of the tables' tensors into partial[0 .. *used) (`slots` at
 // most), in a fixed order.  With `fin` not null the one workgroup of a launch
-// that has just one writes the result itself (*used = 0).
-hipError_t launch_sumsq(const TensorTable& t, int dt, double* partial, int slots, const NormOut* fin, int cus,
-                        int* used, void* stream);
+// that has just one writes the result itself (*used = 0).  bytes: those of all
+// the call's tensors.
+hipError_t launch_sumsq(const TensorTable& t, int dt, int64_t bytes, double* partial, int slots, const NormOut* fin,
+                        int cus, int* used, void* stream);
 hipError_t launch_norm_units(const NormUnitArgs* units, int n, int world, int grad_dt, int fp32_reduce,
                              const ReduceScalars& rs, double* partial, int slots, int cus, int* used, void* stream);
 hipError_t launch_norm_finish(const double* partial, int n, const NormOut& out, void* stream);
-hipError_t launch_clip(const TensorTable& t, int dt, const float* coef, void* stream);
+hipError_t launch_clip(const TensorTable& t, int dt, int64_t bytes, const float* coef, void* stream);
 
 }  // namespace fsdp

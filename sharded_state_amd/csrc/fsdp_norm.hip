@@ -23,6 +23,12 @@ namespace fsdp {
 // an address off the 16-byte grid costs a second cache line now and then).
 typedef u32x4 u32x4_any __attribute__((aligned(1)));
 
+// 16 bytes at p, with the non-temporal hint or without.
+template <bool NT>
+__device__ __forceinline__ u32x4 ld_any(const char* p) {
+    if constexpr (NT) return __builtin_nontemporal_load((const u32x4_any*)p);
+    else return *(const u32x4_any*)p;
+}
 __device__ __forceinline__ double sq(float x, double acc) {
     const double d = (double)x;
     return __builtin_fma(d, d, acc);
@@ -80,7 +86,7 @@ __device__ __forceinline__ int tensor_of(const TensorTable& T, int64_t c) {
     return lo;
 }
 
-template <int F, bool FINISH>
+template <int F, bool STREAM, bool FINISH>
 __global__ __launch_bounds__(kThreads) void k_sumsq(TensorTable T, double* __restrict__ partial, NormOut fin) {
     constexpr int kEs = F == FSDP_F32 ? 4 : 2;
     constexpr int64_t kElems = kSumChunkBytes / kEs;
@@ -95,7 +101,7 @@ __global__ __launch_bounds__(kThreads) void k_sumsq(TensorTable T, double* __res
         if (n >= kElems) {
             u32x4 v[kU];
 #pragma unroll
-            for (int u = 0; u < kU; ++u) v[u] = *(const u32x4_any*)(p + ((int64_t)u * kThreads + threadIdx.x) * 16);
+            for (int u = 0; u < kU; ++u) v[u] = ld_any<STREAM>(p + ((int64_t)u * kThreads + threadIdx.x) * 16);
 #pragma unroll
             for (int u = 0; u < kU; ++u) sq16<F>(v[u], a, b);
         } else {
@@ -111,23 +117,95 @@ __global__ __launch_bounds__(kThreads) void k_sumsq(TensorTable T, double* __res
     }
 }
 
-__global__ __launch_bounds__(kThreads) void k_norm_finish(const double* __restrict__ partial, int n, NormOut o) {
+// 1024 lanes with their loads first: the launch is a chain of latencies.
+constexpr int kFinishThreads = 1024;
+constexpr int kFinishU = kNormSlots / kFinishThreads;
+__global__ __launch_bounds__(kFinishThreads) void k_norm_finish(const double* __restrict__ partial, int n, NormOut o) {
     double s = 0.0;
-    for (int i = threadIdx.x; i < n; i += kThreads) s += partial[i];
-    s = block_sum<kThreads>(s);
+    for (int i0 = threadIdx.x; i0 < n; i0 += kFinishThreads * kFinishU) {
+        double v[kFinishU];
+#pragma unroll
+        for (int u = 0; u < kFinishU; ++u) v[u] = i0 + u * kFinishThreads < n ? partial[i0 + u * kFinishThreads] : 0.0;
+#pragma unroll
+        for (int u = 0; u < kFinishU; ++u) s += v[u];
+    }
+    s = block_sum<kFinishThreads>(s);
     if (threadIdx.x == 0) write_norm(s, o);
+}
+
+// 8 consecutive elements of format F at p, at any address, with the non-temporal hint.
+template <int F>
+__device__ __forceinline__ void load8_any(const char* p, float (&x)[8]) {
+    const u32x4 a = ld_any<true>(p);
+    uint32_t w[8] = {a.x, a.y, a.z, a.w};
+    if constexpr (F == FSDP_F32) {
+        const u32x4 b = ld_any<true>(p + 16);
+        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if constexpr (F == FSDP_F32) x[k] = __uint_as_float(w[k]);
+        else x[k] = to_f32<F>(k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xffffu);
+    }
+}
+
+// The fold of reduce8 over blocks at any address (four ranks' loads at a time).
+template <int NW, int GF, bool FP32R, typename GP>
+__device__ __forceinline__ void reduce8_any(const GP& gp, int world, int64_t vi, float (&acc)[8]) {
+    constexpr int kBytes = GF == FSDP_F32 ? 32 : 16;
+    const int n = NW > 0 ? NW : world;
+    load8_any<GF>((const char*)gp(0) + vi * kBytes, acc);
+    int q = 1;
+    for (; q + 4 <= n; q += 4) {
+        float x[4][8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load8_any<GF>((const char*)gp(q + j) + vi * kBytes, x[j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[k] = fold<NW, GF, FP32R>(acc[k], x[j][k]);
+    }
+    for (; q < n; ++q) {
+        float x[8];
+        load8_any<GF>((const char*)gp(q) + vi * kBytes, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] = fold<NW, GF, FP32R>(acc[k], x[k]);
+    }
+}
+
+template <int F>
+__device__ __forceinline__ void store8_any(char* p, const float (&x)[8]) {
+    if constexpr (F == FSDP_F32) {
+        u32x4 a, b;
+        a.x = __float_as_uint(x[0]); a.y = __float_as_uint(x[1]);
+        a.z = __float_as_uint(x[2]); a.w = __float_as_uint(x[3]);
+        b.x = __float_as_uint(x[4]); b.y = __float_as_uint(x[5]);
+        b.z = __float_as_uint(x[6]); b.w = __float_as_uint(x[7]);
+        *(u32x4_any*)p = a;
+        *(u32x4_any*)(p + 16) = b;
+    } else {
+        u32x4 a;
+        a.x = from_f32<F>(x[0]) | (from_f32<F>(x[1]) << 16);
+        a.y = from_f32<F>(x[2]) | (from_f32<F>(x[3]) << 16);
+        a.z = from_f32<F>(x[4]) | (from_f32<F>(x[5]) << 16);
+        a.w = from_f32<F>(x[6]) | (from_f32<F>(x[7]) << 16);
+        *(u32x4_any*)p = a;
+    }
 }
 
 // The sum over the averaged gradient of a table of units: the reduce-scatter's
 // fold (fsdp_device.h) with the squares added as its epilogue, and the shard
 // stored where the caller wants it.  Vectors in the group layout for an fp32
-// shard, 8 consecutive elements for a 16-bit one, as k_reduce_scatter has them.
+// shard, 8 consecutive elements for a 16-bit one, as k_reduce_scatter has them;
+// a unit with a buffer off the 16-byte grid (a shard of an odd size) goes 8
+// consecutive elements at a time through accesses at any address.
 template <int NW, int GF, bool FP32R>
 __global__ __launch_bounds__(kThreads) void k_norm_units(NormUnits<NW> B, ReduceScalars rs,
                                                          double* __restrict__ partial) {
     constexpr int OF = (FP32R || GF == FSDP_F32) ? FSDP_F32 : GF;
     constexpr bool kGroup = OF == FSDP_F32;
     const int64_t tiles = B.tile_begin[B.count];
+    const int world = NW > 0 ? NW : B.world;
     double a = 0.0, b = 0.0;
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
         int lo = 0, hi = B.count - 1;
@@ -137,7 +215,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_units(NormUnits<NW> B, Reduce
             else hi = mid - 1;
         }
         const int u = lo;
-        const auto gp = [&](int q) -> const void* { return B.g[u][q]; };
+        const auto gp = [&](int q) -> const void* { return B.g[u * world + q]; };
         const int64_t j = t - B.tile_begin[u];
         const int64_t nvec = B.nvec[u];
         const int64_t tv = (nvec + kThreads - 1) / kThreads;
@@ -146,10 +224,12 @@ __global__ __launch_bounds__(kThreads) void k_norm_units(NormUnits<NW> B, Reduce
             const int64_t vi = j * kThreads + threadIdx.x;
             if (vi < nvec) {
                 float x[8];
-                reduce8<NW, GF, FP32R, true, kGroup>(gp, B.world, vi, x);
+                if (B.wide[u]) reduce8<NW, GF, FP32R, true, kGroup>(gp, world, vi, x);
+                else reduce8_any<NW, GF, FP32R>(gp, world, vi, x);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) x[k] = finish<NW, GF, FP32R>(x[k], rs);
-                if (out) store8x<OF, kGroup>(out, vi, x);
+                if (out && B.wide[u]) store8x<OF, kGroup>(out, vi, x);
+                else if (out) store8_any<OF>((char*)out + vi * (OF == FSDP_F32 ? 32 : 16), x);
 #pragma unroll
                 for (int k = 0; k < 8; k += 2) {
                     a = sq(x[k], a);
@@ -159,7 +239,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_units(NormUnits<NW> B, Reduce
         } else {
             const int64_t i = nvec * 8 + (j - tv) * kThreads + threadIdx.x;
             if (i < B.S[u]) {
-                const float x = finish<NW, GF, FP32R>(reduce1<NW, GF, FP32R>(gp, B.world, i), rs);
+                const float x = finish<NW, GF, FP32R>(reduce1<NW, GF, FP32R>(gp, world, i), rs);
                 if (out) store1<OF>(out, i, x);
                 a = sq(x, a);
             }
@@ -182,7 +262,12 @@ __device__ __forceinline__ uint32_t scaled(uint32_t bits, float c) {
 // Clipping in place: one 16-byte vector a lane, as the segmented copies.  A
 // coefficient of exactly 1 leaves every element as it is, so those launches
 // end after one scalar load; a NaN coefficient (a NaN norm) is applied.
-template <int F>
+// STREAM (see streams()): a wave's stores go out as one span with the streamed
+// policy, and the sum's loads carry the non-temporal hint.  Norm and clip of the
+// 13B block's 629 MB 347 -> 283 us (norm 108 -> 94, 6.7 TB/s), of 246 MB 145 ->
+// 120; of 39 MB, which the memory-side cache keeps from the sum to the clip,
+// 26.0 us without and 28 with.
+template <int F, bool STREAM>
 __global__ __launch_bounds__(kThreads) void k_clip(TensorTable T, const float* __restrict__ coef) {
     constexpr int kEs = F == FSDP_F32 ? 4 : 2;
     constexpr int64_t kElems = kClipChunkBytes / kEs;
@@ -206,7 +291,9 @@ __global__ __launch_bounds__(kThreads) void k_clip(TensorTable T, const float* _
             }
             u32x4 r;
             r.x = w[0]; r.y = w[1]; r.z = w[2]; r.w = w[3];
-            *(u32x4_any*)(p + threadIdx.x * 16) = r;
+            const int l = threadIdx.x & 63;
+            if (STREAM && ((uintptr_t)p & 15) == 0) st16_wave(p + (threadIdx.x - l) * 16, l, r);
+            else *(u32x4_any*)(p + threadIdx.x * 16) = r;
         }
         // fewer than one vector's elements are left
         const int64_t i = nv * (16 / kEs) + threadIdx.x;
@@ -218,32 +305,44 @@ __global__ __launch_bounds__(kThreads) void k_clip(TensorTable T, const float* _
 }
 
 // ----------------------------------------------------------------- launchers
-// Workgroups of a summing launch: 8 a CU (2048 lanes, the CU's limit).
-static int sum_grid(int64_t chunks, int slots, int cus) {
-    int64_t g = (int64_t)cus * 8;
+// Whether a call's tensors are more than the memory-side cache (256 MB) could
+// hand from one pass to the next.
+static bool streams(int64_t bytes) { return bytes > (int64_t(128) << 20); }
+
+// Workgroups of a summing launch, `per` a CU.  A list: 4 (13B block, non-temporal
+// loads: 93.7 us, with 8 96.0).  Units: 8 for few ranks, whose lanes have few
+// loads each, 4 from four ranks on, 3 where eight ranks' shards are stored too
+// (us with 3, 4, 8: N = 1 fp32 92.3, 75.4, 62.2; N = 2 bf16 97.0, 80.1, 64.2; N = 4
+// fp16 40.8, 38.0, 39.2; N = 8 bf16 271.6, 264.3 (6.5 TB/s), 278.9, and with its
+// shard stored 343.9, 361.6, 380.9).
+static int units_per_cu(int world, bool store) { return world < 4 ? 8 : world >= 8 && store ? 3 : 4; }
+static int sum_grid(int64_t chunks, int slots, int cus, int per) {
+    int64_t g = (int64_t)cus * per;
     if (g > slots) g = slots;
     if (g > chunks) g = chunks;
     return g < 1 ? 1 : (int)g;
 }
 
-hipError_t launch_sumsq(const TensorTable& t, int dt, double* partial, int slots, const NormOut* fin, int cus,
-                        int* used, void* stream) {
+template <int F>
+static void sumsq(const TensorTable& t, double* partial, int g, const NormOut* fin, bool stream, hipStream_t st) {
+    const NormOut none{};
+    if (fin) launch(k_sumsq<F, false, true>, dim3(1), dim3(kThreads), st, t, partial, *fin);
+    else if (stream) launch(k_sumsq<F, true, false>, dim3(g), dim3(kThreads), st, t, partial, none);
+    else launch(k_sumsq<F, false, false>, dim3(g), dim3(kThreads), st, t, partial, none);
+}
+
+hipError_t launch_sumsq(const TensorTable& t, int dt, int64_t bytes, double* partial, int slots, const NormOut* fin,
+                        int cus, int* used, void* stream) {
     const int64_t chunks = t.chunk_begin[t.count];
     *used = 0;
     if (chunks <= 0) return hipSuccess;
     hipStream_t st = (hipStream_t)stream;
-    const int g = sum_grid(chunks, slots, cus);
-    const NormOut none{};
-    if (g == 1 && fin) {
-        if (dt == FSDP_F32) launch(k_sumsq<FSDP_F32, true>, dim3(1), dim3(kThreads), st, t, partial, *fin);
-        else if (dt == FSDP_F16) launch(k_sumsq<FSDP_F16, true>, dim3(1), dim3(kThreads), st, t, partial, *fin);
-        else launch(k_sumsq<FSDP_BF16, true>, dim3(1), dim3(kThreads), st, t, partial, *fin);
-        return hipGetLastError();
-    }
-    *used = g;
-    if (dt == FSDP_F32) launch(k_sumsq<FSDP_F32, false>, dim3(g), dim3(kThreads), st, t, partial, none);
-    else if (dt == FSDP_F16) launch(k_sumsq<FSDP_F16, false>, dim3(g), dim3(kThreads), st, t, partial, none);
-    else launch(k_sumsq<FSDP_BF16, false>, dim3(g), dim3(kThreads), st, t, partial, none);
+    const int g = sum_grid(chunks, slots, cus, 4);
+    if (g > 1) fin = nullptr;
+    *used = fin ? 0 : g;
+    if (dt == FSDP_F32) sumsq<FSDP_F32>(t, partial, g, fin, streams(bytes), st);
+    else if (dt == FSDP_F16) sumsq<FSDP_F16>(t, partial, g, fin, streams(bytes), st);
+    else sumsq<FSDP_BF16>(t, partial, g, fin, streams(bytes), st);
     return hipGetLastError();
 }
 
@@ -251,7 +350,7 @@ template <int NW>
 static hipError_t norm_units_all(const NormUnitArgs* units, int n, int world, int grad_dt, int fp32_reduce,
                                  const ReduceScalars& rs, double* partial, int slots, int cus, int* used,
                                  void* stream) {
-    constexpr int kMax = NormUnits<NW>::kMax;
+    const int kMax = norm_units_max(world);
     const int launches = (n + kMax - 1) / kMax;
     const int per = slots / (launches > 0 ? launches : 1);
     const bool f32r = fp32_reduce || grad_dt == FSDP_F32;
@@ -263,18 +362,19 @@ static hipError_t norm_units_all(const NormUnitArgs* units, int n, int world, in
         int64_t tiles = 0;
         for (int k = 0; k < c; ++k) {
             const NormUnitArgs& a = units[done + k];
-            const int64_t nvec = a.nvec & ~int64_t(63);   // whole groups; the rest joins the tail
+            const int64_t nvec = a.S / 8 & ~int64_t(63);  // whole groups; the rest joins the tail
             B.tile_begin[k] = tiles;
             B.nvec[k] = nvec;
             B.S[k] = a.S;
             B.out[k] = a.out;
-            for (int q = 0; q < world; ++q) B.g[k][q] = a.grads[q];
+            B.wide[k] = a.wide;
+            for (int q = 0; q < world; ++q) B.g[k * world + q] = a.grads[q];
             tiles += (nvec + kThreads - 1) / kThreads + (a.S - 8 * nvec + kThreads - 1) / kThreads;
         }
         B.count = c;
         B.tile_begin[c] = tiles;
         if (tiles == 0) continue;
-        const dim3 g((unsigned)sum_grid(tiles, per, cus)), th(kThreads);
+        const dim3 g((unsigned)sum_grid(tiles, per, cus, units_per_cu(world, units[done].out != nullptr))), th(kThreads);
         hipStream_t st = (hipStream_t)stream;
         double* out = partial + *used;
         if (grad_dt == FSDP_F32) launch(k_norm_units<NW, FSDP_F32, true>, g, th, st, B, rs, out);
@@ -301,19 +401,25 @@ hipError_t launch_norm_units(const NormUnitArgs* units, int n, int world, int gr
 }
 
 hipError_t launch_norm_finish(const double* partial, int n, const NormOut& out, void* stream) {
-    launch(k_norm_finish, dim3(1), dim3(kThreads), (hipStream_t)stream, partial, n, out);
+    launch(k_norm_finish, dim3(1), dim3(kFinishThreads), (hipStream_t)stream, partial, n, out);
     return hipGetLastError();
 }
 
-hipError_t launch_clip(const TensorTable& t, int dt, const float* coef, void* stream) {
+template <int F>
+static void clip(const TensorTable& t, const float* coef, dim3 g, bool stream, hipStream_t st) {
+    if (stream) launch(k_clip<F, true>, g, dim3(kThreads), st, t, coef);
+    else launch(k_clip<F, false>, g, dim3(kThreads), st, t, coef);
+}
+
+hipError_t launch_clip(const TensorTable& t, int dt, int64_t bytes, const float* coef, void* stream) {
     const int64_t chunks = t.chunk_begin[t.count];
     if (chunks <= 0) return hipSuccess;
     // a launch holds fewer than 2^32 work items; beyond 2^22 workgroups they loop
-    const dim3 g((unsigned)(chunks < (1 << 22) ? chunks : (1 << 22))), th(kThreads);
+    const dim3 g((unsigned)(chunks < (1 << 22) ? chunks : (1 << 22)));
     hipStream_t st = (hipStream_t)stream;
-    if (dt == FSDP_F32) launch(k_clip<FSDP_F32>, g, th, st, t, coef);
-    else if (dt == FSDP_F16) launch(k_clip<FSDP_F16>, g, th, st, t, coef);
-    else launch(k_clip<FSDP_BF16>, g, th, st, t, coef);
+    if (dt == FSDP_F32) clip<FSDP_F32>(t, coef, g, streams(bytes), st);
+    else if (dt == FSDP_F16) clip<FSDP_F16>(t, coef, g, streams(bytes), st);
+    else clip<FSDP_BF16>(t, coef, g, streams(bytes), st);
     return hipGetLastError();
 }
 

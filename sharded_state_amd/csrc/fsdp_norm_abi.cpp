@@ -49,6 +49,12 @@ int check_workspace(const char* fn, void* ws, std::vector<Range>& outs) {
     return FSDP_OK;
 }
 
+int64_t total_bytes(const std::vector<Range>& rs) {
+    uint64_t n = 0;
+    for (const Range& r : rs) n += r.n;
+    return (int64_t)n;
+}
+
 // Validate a list of tensors and put it into tables, format by format.
 int tensor_tables(const char* fn, const void* const* ptrs, const int64_t* numels, const fsdp_dtype* dts, int32_t n,
                   int64_t chunk_bytes, std::vector<TensorTable>& tables, std::vector<int>& formats,
@@ -112,7 +118,7 @@ int fsdp_grad_norm(const void* const* srcs, const int64_t* numels, const fsdp_dt
         (void)hipGetLastError();
         for (size_t t = 0; t < tables.size(); ++t) {
             int got = 0;
-            hipError_t e = launch_sumsq(tables[t], formats[t], partial + used, kNormSlots / (int)tables.size(),
+            hipError_t e = launch_sumsq(tables[t], formats[t], total_bytes(ins), partial + used, kNormSlots / (int)tables.size(),
                                         tables.size() == 1 ? &o : nullptr, cus, &got, stream);
             if (e != hipSuccess) return hip_fail(e, "norm launch");
             if (got == 0) return ok();          // that launch wrote the result itself
@@ -151,7 +157,7 @@ int fsdp_grad_norm_units(const fsdp_norm_unit* units, int32_t n_units, int32_t w
             bool vec = !u.grad_shard || aligned16(u.grad_shard);
             for (int q = 0; q < world; ++q) vec = vec && aligned16(blocks[k][q]);
             if (u.grad_shard) outs.push_back(range(u.grad_shard, u.shard_numel, dt_size(out_dt)));
-            args.push_back(NormUnitArgs{blocks[k].data(), u.grad_shard, u.shard_numel, vec ? u.shard_numel / 8 : 0});
+            args.push_back(NormUnitArgs{blocks[k].data(), u.grad_shard, u.shard_numel, vec});
         }
         if (!disjoint(outs, ins)) return fail(FSDP_E_ALIAS, "%s: an output overlaps an input or another output", fn);
         const int launches = ((int)args.size() + norm_units_max(world) - 1) / norm_units_max(world);
@@ -203,7 +209,7 @@ int fsdp_clip_grads(void* const* tensors, const int64_t* numels, const fsdp_dtyp
             return fail(FSDP_E_ALIAS, "%s: a tensor overlaps another one or the coefficient", fn);
         (void)hipGetLastError();
         for (size_t t = 0; t < tables.size(); ++t) {
-            hipError_t e = launch_clip(tables[t], formats[t], coef, stream);
+            hipError_t e = launch_clip(tables[t], formats[t], total_bytes(outs), coef, stream);
             if (e != hipSuccess) return hip_fail(e, "clip launch");
         }
         return ok();
