@@ -37,6 +37,20 @@ def _on(stream):
     return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext()
 
 
+def _issue(name, device, stream, *args):
+    """Call entry point `name` with `args` and the stream (the device's current
+    one for None) as its last argument, with `device` current."""
+    raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+    fn = getattr(N.lib(), name)
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, raw)
+    if rc != N.OK:
+        check(name, rc)
+
+
 def _dev(t, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a tensor" % name)

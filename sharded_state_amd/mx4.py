@@ -17,13 +17,11 @@ axes that it sums over and takes W quantised along its columns
 (``fsdp_mx4_quantize(w, form="columns")``).  Quantisation itself is passed
 through unchanged by the gradients.
 """
-import ctypes
-
 import torch
 
 from . import _native as N
-from ._native import check, ptr_array
-from .api import _dev, _on, _same_device, _stream, dtype_code
+from ._native import ptr_array
+from .api import _dev, _issue, _on, dtype_code
 
 BLOCK = 32
 
@@ -56,8 +54,11 @@ class Mx4:
     @classmethod
     def empty(cls, rows, cols, device="cuda"):
         nb = _blocks(cols)
-        return cls(torch.empty((rows, nb * 16), dtype=torch.uint8, device=device),
-                   torch.empty((rows, nb), dtype=torch.uint8, device=device), cols)
+        self = object.__new__(cls)               # what is allocated here needs no check
+        self.codes = torch.empty((rows, nb * 16), dtype=torch.uint8, device=device)
+        self.scales = torch.empty((rows, nb), dtype=torch.uint8, device=device)
+        self.rows, self.cols = rows, cols
+        return self
 
     @property
     def device(self):
@@ -72,27 +73,40 @@ class Mx4:
 
 
 def _matrix(t, name):
-    """A device tensor as (tensor, rows, cols, row stride); 1-D is one row."""
+    """A device tensor as (rows, columns, row stride); 1-D is one row."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a tensor" % name)
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("%s must be a device tensor, got %s" % (name, t.device))
-    if t.dim() == 1:
-        t = t.unsqueeze(0)
-    if t.dim() != 2:
-        raise ValueError("%s must have one or two dimensions, got %d" % (name, t.dim()))
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1 or rows > 1 and cols > 0 and t.stride(0) < cols:
+    shape = t.shape
+    if len(shape) == 1:
+        cols = shape[0]
+        if cols > 1 and t.stride(0) != 1:
+            raise ValueError("%s must have its elements next to each other" % name)
+        return 1, cols, cols
+    if len(shape) != 2:
+        raise ValueError("%s must have one or two dimensions, got %d" % (name, len(shape)))
+    rows, cols = shape
+    ld, step = t.stride()
+    if cols > 1 and step != 1 or rows > 1 and cols > 0 and ld < cols:
         raise ValueError("%s must have its rows' elements next to each other" % name)
-    return t, rows, cols, t.stride(0) if rows > 1 else cols
+    return rows, cols, ld if rows > 1 else cols
 
 
-def _result(out, rows, cols):
-    """A product's output as (tensor, row stride)."""
+def _result(out, rows, cols, dtype, device, stream):
+    """A product's output, allocated where none is given, as (tensor, row stride)."""
+    if out is None:
+        with _on(stream):
+            return torch.empty((rows, cols), dtype=dtype, device=device), cols
     if not isinstance(out, torch.Tensor) or tuple(out.shape) != (rows, cols):
         raise ValueError("out must be a matrix of %d x %d" % (rows, cols))
-    out, _, _, ldo = _matrix(out, "out")
-    return out, ldo
+    return out, _matrix(out, "out")[2]
+
+
+def _one_device(device, *tensors):
+    for t in tensors:
+        if t.device != device:
+            raise ValueError("all tensors must be on one device, got %s and %s" % (device, t.device))
 
 
 def _target(out, rows, cols, device, stream, name):
@@ -115,16 +129,18 @@ def fsdp_mx4_quantize(src, out=None, out_t=None, form="rows", stream=None):
         raise ValueError("form must be rows, columns or both, got %r" % (form,))
     if (out is not None and form == "columns") or (out_t is not None and form == "rows"):
         raise ValueError("form %r has no such output" % form)
-    src, rows, cols, ld = _matrix(src, "src")
+    rows, cols, ld = _matrix(src, "src")
     device = src.device
     dt = dtype_code(src.dtype)
-    a = _target(out, rows, cols, device, stream, "out") if form != "columns" else None
-    t = _target(out_t, cols, rows, device, stream, "out_t") if form != "rows" else None
-    p = [ctypes.c_void_p(x.data_ptr()) if x is not None else None
-         for q in (a, t) for x in ((q.codes, q.scales) if q is not None else (None, None))]
-    with torch.cuda.device(device):
-        check("fsdp_mx4_quantize", N.lib().fsdp_mx4_quantize(ctypes.c_void_p(src.data_ptr()), dt, rows, cols, ld, *p,
-                                                             _stream(stream, device)))
+    a = t = None
+    p = [None, None, None, None]
+    if form != "columns":
+        a = _target(out, rows, cols, device, stream, "out")
+        p[0], p[1] = a.codes.data_ptr(), a.scales.data_ptr()
+    if form != "rows":
+        t = _target(out_t, cols, rows, device, stream, "out_t")
+        p[2], p[3] = t.codes.data_ptr(), t.scales.data_ptr()
+    _issue("fsdp_mx4_quantize", device, stream, src.data_ptr(), dt, rows, cols, ld, *p)
     return a if form == "rows" else t if form == "columns" else (a, t)
 
 
@@ -150,11 +166,9 @@ def fsdp_mx4_gather(shards, full=None, dtype=torch.bfloat16, stream=None):
     _dev(full, "full")
     if full.numel() != world * S:
         raise ValueError("full must hold world*shard = %d elements" % (world * S))
-    _same_device([s.codes for s in shards] + [full])
-    with torch.cuda.device(device):
-        check("fsdp_mx4_gather", N.lib().fsdp_mx4_gather(
-            ptr_array([s.codes.data_ptr() for s in shards]), ptr_array([s.scales.data_ptr() for s in shards]), world,
-            S, dtype_code(full.dtype), ctypes.c_void_p(full.data_ptr()), _stream(stream, device)))
+    _one_device(device, full, *(s.codes for s in shards))
+    _issue("fsdp_mx4_gather", device, stream, ptr_array([s.codes.data_ptr() for s in shards]),
+           ptr_array([s.scales.data_ptr() for s in shards]), world, S, dtype_code(full.dtype), full.data_ptr())
     return full
 
 
@@ -165,12 +179,9 @@ def fsdp_mx4_gather_packed(shards, full=None, stream=None):
     if S % BLOCK:
         raise ValueError("the shard's size %d is not a multiple of %d: the shards' blocks do not join" % (S, BLOCK))
     full = _target(full, 1, world * S, device, stream, "full")
-    _same_device([s.codes for s in shards] + [full.codes])
-    with torch.cuda.device(device):
-        check("fsdp_mx4_gather_packed", N.lib().fsdp_mx4_gather_packed(
-            ptr_array([s.codes.data_ptr() for s in shards]), ptr_array([s.scales.data_ptr() for s in shards]), world,
-            S, ctypes.c_void_p(full.codes.data_ptr()), ctypes.c_void_p(full.scales.data_ptr()),
-            _stream(stream, device)))
+    _one_device(device, full.codes, *(s.codes for s in shards))
+    _issue("fsdp_mx4_gather_packed", device, stream, ptr_array([s.codes.data_ptr() for s in shards]),
+           ptr_array([s.scales.data_ptr() for s in shards]), world, S, full.codes.data_ptr(), full.scales.data_ptr())
     return full
 
 
@@ -204,22 +215,16 @@ def fsdp_mx4_matmul(a, b, out=None, dtype=torch.bfloat16, stream=None):
     for name, x in (("a", a), ("b", b)):
         if not isinstance(x, Mx4):
             raise TypeError("%s must be an Mx4" % name)
-        _dev(x.codes, name)
+        if not x.codes.is_cuda:
+            raise ValueError("%s must be on a device, got %s" % (name, x.device))
     if a.cols != b.cols:
         raise ValueError("a has %d columns, b %d" % (a.cols, b.cols))
     device = a.device
-    if out is None:
-        with _on(stream):
-            out = torch.empty((a.rows, b.rows), dtype=dtype, device=device)
-    res = out
-    out, ldo = _result(out, a.rows, b.rows)
-    _same_device([a.codes, b.codes, out])
-    with torch.cuda.device(device):
-        check("fsdp_mx4_matmul", N.lib().fsdp_mx4_matmul(
-            ctypes.c_void_p(a.codes.data_ptr()), ctypes.c_void_p(a.scales.data_ptr()),
-            ctypes.c_void_p(b.codes.data_ptr()), ctypes.c_void_p(b.scales.data_ptr()), a.rows, b.rows, a.cols,
-            dtype_code(out.dtype), ctypes.c_void_p(out.data_ptr()), ldo, _stream(stream, device)))
-    return res
+    out, ldo = _result(out, a.rows, b.rows, dtype, device, stream)
+    _one_device(device, b.codes, out)
+    _issue("fsdp_mx4_matmul", device, stream, a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
+           b.scales.data_ptr(), a.rows, b.rows, a.cols, dtype_code(out.dtype), out.data_ptr(), ldo)
+    return out
 
 
 def fsdp_mx4_linear(x, w, out=None, stream=None):
@@ -234,18 +239,12 @@ def fsdp_mx4_linear(x, w, out=None, stream=None):
     if x.shape[0] > N.MX4_FEW or x.shape[0] * w.scales.shape[1] > N.MX4_FEW_BLOCKS:
         with _on(stream):
             return fsdp_mx4_matmul(fsdp_mx4_quantize(x, stream=stream), w, out, x.dtype, stream)
-    x, m, k, ldx = _matrix(x, "x")
+    m, k, ldx = _matrix(x, "x")
     device = x.device
-    if out is None:
-        with _on(stream):
-            out = torch.empty((m, w.rows), dtype=x.dtype, device=device)
-    y, ldo = _result(out, m, w.rows)
-    _same_device([x, w.codes, y])
-    with torch.cuda.device(device):
-        check("fsdp_mx4_linear_few", N.lib().fsdp_mx4_linear_few(
-            ctypes.c_void_p(x.data_ptr()), dtype_code(x.dtype), m, k, ldx, ctypes.c_void_p(w.codes.data_ptr()),
-            ctypes.c_void_p(w.scales.data_ptr()), w.rows, dtype_code(y.dtype), ctypes.c_void_p(y.data_ptr()), ldo,
-            _stream(stream, device)))
+    out, ldo = _result(out, m, w.rows, x.dtype, device, stream)
+    _one_device(device, w.codes, out)
+    _issue("fsdp_mx4_linear_few", device, stream, x.data_ptr(), dtype_code(x.dtype), m, k, ldx, w.codes.data_ptr(),
+           w.scales.data_ptr(), w.rows, dtype_code(out.dtype), out.data_ptr(), ldo)
     return out
 
 

@@ -22,8 +22,8 @@ import ctypes
 import torch
 
 from . import _native as N
-from ._native import check, i64_array, ptr_array
-from .api import _dev, _grads, _on, _same_device, _stream, dtype_code
+from ._native import i64_array, ptr_array
+from .api import _dev, _grads, _issue, _on, _same_device, dtype_code
 
 _WS = N.NORM_WORKSPACE_BYTES
 
@@ -62,8 +62,7 @@ class GradNorm:
         """(max_norm, sumsq, norm, coef) of a call, and the workspace's address."""
         p = self._buf.data_ptr()
         self.has_coef = max_norm is not None
-        return (float(max_norm) if self.has_coef else 0.0, ctypes.c_void_p(p), ctypes.c_void_p(p + 8),
-                ctypes.c_void_p(p + 12 if self.has_coef else None)), ctypes.c_void_p(p + 16)
+        return (float(max_norm) if self.has_coef else 0.0, p, p + 8, p + 12 if self.has_coef else None), p + 16
 
 
 def _out(out, device, stream):
@@ -96,7 +95,10 @@ def clip_coef(clip):
 
 
 def _list(tensors, name):
-    tensors = [_dev(t, "%s[%d]" % (name, i)) for i, t in enumerate(tensors)]
+    tensors = list(tensors)
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+            _dev(t, "%s[%d]" % (name, i))        # says what is wrong
     n = len(tensors)
     return (tensors, ptr_array([t.data_ptr() for t in tensors]), i64_array([t.numel() for t in tensors]),
             (ctypes.c_int32 * max(n, 1))(*[dtype_code(t.dtype) for t in tensors]), n)
@@ -113,9 +115,8 @@ def fsdp_grad_norm(tensors, max_norm=None, out=None, stream=None):
     device = tensors[0].device if tensors else out.device
     _same_device(tensors)
     out = _out(out, device, stream)
-    with torch.cuda.device(device):
-        outs, ws = out._args(max_norm)
-        check("fsdp_grad_norm", N.lib().fsdp_grad_norm(ptrs, numels, dts, n, *outs, ws, _stream(stream, device)))
+    outs, ws = out._args(max_norm)
+    _issue("fsdp_grad_norm", device, stream, ptrs, numels, dts, n, *outs, ws)
     return out
 
 
@@ -160,11 +161,9 @@ def fsdp_grad_norm_units(units, rank, fp32_reduce, max_norm=None, out=None, stre
     _same_device(tensors)
     device = tensors[0].device
     out = _out(out, device, stream)
-    with torch.cuda.device(device):
-        outs, ws = out._args(max_norm)
-        check("fsdp_grad_norm_units", N.lib().fsdp_grad_norm_units(
-            table, len(units), world, int(rank), dtype_code(gdt), int(bool(fp32_reduce)), *outs, ws,
-            _stream(stream, device)))
+    outs, ws = out._args(max_norm)
+    _issue("fsdp_grad_norm_units", device, stream, table, len(units), world, int(rank), dtype_code(gdt),
+           int(bool(fp32_reduce)), *outs, ws)
     return out
 
 
@@ -177,10 +176,8 @@ def fsdp_grad_norm_combine(sumsqs, max_norm=None, out=None, stream=None):
         raise TypeError("sumsqs must be float64")
     device = sumsqs.device
     out = _out(out, device, stream)
-    with torch.cuda.device(device):
-        outs, _ = out._args(max_norm)
-        check("fsdp_grad_norm_combine", N.lib().fsdp_grad_norm_combine(
-            ctypes.c_void_p(sumsqs.data_ptr()), sumsqs.numel(), *outs, _stream(stream, device)))
+    outs, _ = out._args(max_norm)
+    _issue("fsdp_grad_norm_combine", device, stream, sumsqs.data_ptr(), sumsqs.numel(), *outs)
     return out
 
 
@@ -192,7 +189,5 @@ def fsdp_clip_grads(tensors, clip, stream=None):
     coef = clip_coef(clip)
     _same_device(tensors + [coef])
     device = coef.device
-    with torch.cuda.device(device):
-        check("fsdp_clip_grads", N.lib().fsdp_clip_grads(ptrs, numels, dts, n, ctypes.c_void_p(coef.data_ptr()),
-                                                         _stream(stream, device)))
+    _issue("fsdp_clip_grads", device, stream, ptrs, numels, dts, n, coef.data_ptr())
     return tensors
