@@ -430,8 +430,6 @@ FSDP_API int fsdp_step_units_clipped(const fsdp_unit* units, int32_t n_units, in
  * 16-byte aligned (FSDP_E_INVAL otherwise).
  * ------------------------------------------------------------------------ */
 #define FSDP_MX4_MAX_K (1 << 23)   /* longest summed axis of a product */
-#define FSDP_MX4_FEW 16            /* most tokens of fsdp_mx4_linear_few */
-#define FSDP_MX4_FEW_BLOCKS 2048   /* most blocks of its x, m * ceil(k / 32) */
 
 /* Quantise src (rows x cols of dt, ld elements from row to row, any alignment):
  * with codes and scales not NULL in blocks along its rows, with codes_t and
@@ -463,14 +461,32 @@ FSDP_API int fsdp_mx4_matmul(const void* a_codes, const void* a_scales, const vo
                              const void* b_scales, int64_t m, int64_t n, int64_t k, fsdp_dtype out_dt,
                              void* out, int64_t ldo, void* stream);
 
-/* y = x W^T for m <= FSDP_MX4_FEW tokens with m * ceil(k / 32) <=
- * FSDP_MX4_FEW_BLOCKS (FSDP_E_SIZE otherwise) in one launch: x [m][k] of x_dt (ldx
- * elements from row to row, any alignment) is quantised along k on the way, as
- * fsdp_mx4_quantize does it, and multiplied by W of n rows and k columns; the
- * result is that of the two calls up to the order of the fp32 sums. */
-FSDP_API int fsdp_mx4_linear_few(const void* x, fsdp_dtype x_dt, int64_t m, int64_t k, int64_t ldx,
-                                 const void* w_codes, const void* w_scales, int64_t n, fsdp_dtype out_dt,
-                                 void* out, int64_t ldo, void* stream);
+/* y = x W^T: x [m][k] of x_dt (ldx elements from row to row, any alignment) is
+ * quantised along k as fsdp_mx4_quantize does it, and multiplied by W of n rows
+ * and k columns into out [m][n].  For a few tokens that is one launch, whose
+ * result is that of the two calls up to the order of the fp32 sums; else x's
+ * blocks lie in the workspace (device, 16-byte aligned, at least
+ * fsdp_mx4_linear_workspace(m, k) bytes, which may be 0: then it may be NULL;
+ * -1 for sizes that the call refuses).  Calls that may run at the same time,
+ * replays of two captured graphs among them, need a workspace each. */
+FSDP_API int64_t fsdp_mx4_linear_workspace(int64_t m, int64_t k);
+FSDP_API int fsdp_mx4_linear(const void* x, fsdp_dtype x_dt, int64_t m, int64_t k, int64_t ldx,
+                             const void* w_codes, const void* w_scales, int64_t n, fsdp_dtype out_dt,
+                             void* out, int64_t ldo, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Gradients of y = x W^T from dy [m][n] and x [m][k]: dx [m][k] = dy W and
+ * dw [n][k] = dy^T x, each the product of its operands quantised along the axis
+ * that it sums over (W, as wt, along its columns: a matrix of k rows and n
+ * columns).  dx or dw may be NULL: not wanted (then wt, or x, may be NULL).
+ * m = 0 gives dw zeros.  Workspace as in fsdp_mx4_linear, at least
+ * fsdp_mx4_linear_grads_workspace(...) bytes. */
+FSDP_API int64_t fsdp_mx4_linear_grads_workspace(int64_t m, int64_t n, int64_t k, int32_t want_dx,
+                                                 int32_t want_dw);
+FSDP_API int fsdp_mx4_linear_grads(const void* dy, fsdp_dtype dy_dt, int64_t lddy, const void* x,
+                                   fsdp_dtype x_dt, int64_t ldx, int64_t m, int64_t n, int64_t k,
+                                   const void* wt_codes, const void* wt_scales, fsdp_dtype dx_dt, void* dx,
+                                   int64_t lddx, fsdp_dtype dw_dt, void* dw, int64_t lddw, void* workspace,
+                                   int64_t workspace_bytes, void* stream);
 
 /* Per-tensor views of the full buffer.  [P3] "The FSDP Unit" (use_orig_params):
  * tensor k is full[off_k : off_k + numel_k]; the padding belongs to no view.

@@ -15,7 +15,6 @@ OK, E_INVAL, E_DTYPE, E_SIZE, E_ALIAS, E_HIP, E_IO, E_FORMAT = 0, -1, -2, -3, -4
 MAX_WORLD = 128
 ABI_VERSION = 10
 NORM_WORKSPACE_BYTES = 32 << 10
-MX4_FEW, MX4_FEW_BLOCKS = 16, 2048
 OFFLOAD_SCRATCH_BYTES = 32 << 20
 OPT_ADAMW, OPT_SGD, OPT_ADAMAX, OPT_ADADELTA = 0, 1, 2, 3
 
@@ -183,8 +182,15 @@ def lib():
     L.fsdp_mx4_gather.argtypes = [vpp, vpp, i32, i64, i32, vp, vp]
     L.fsdp_mx4_gather_packed.restype = ctypes.c_int
     L.fsdp_mx4_gather_packed.argtypes = [vpp, vpp, i32, i64, vp, vp, vp]
-    L.fsdp_mx4_linear_few.restype = ctypes.c_int
-    L.fsdp_mx4_linear_few.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, i32, vp, i64, vp]
+    L.fsdp_mx4_linear_workspace.restype = i64
+    L.fsdp_mx4_linear_workspace.argtypes = [i64, i64]
+    L.fsdp_mx4_linear.restype = ctypes.c_int
+    L.fsdp_mx4_linear.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, i32, vp, i64, vp, i64, vp]
+    L.fsdp_mx4_linear_grads_workspace.restype = i64
+    L.fsdp_mx4_linear_grads_workspace.argtypes = [i64, i64, i64, i32, i32]
+    L.fsdp_mx4_linear_grads.restype = ctypes.c_int
+    L.fsdp_mx4_linear_grads.argtypes = [vp, i32, i64, vp, i32, i64, i64, i64, i64, vp, vp, i32, vp, i64, i32, vp, i64,
+                                        vp, i64, vp]
     L.fsdp_mx4_matmul.restype = ctypes.c_int
     L.fsdp_mx4_matmul.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, vp, i64, vp]
     L.fsdp_unshard_gather.restype = ctypes.c_int

@@ -41,6 +41,7 @@ struct Mx4Product {
 };
 hipError_t launch_mx4_matmul(const Mx4Product& p);
 
+constexpr int kMx4Few = 16;                              // most tokens of launch_mx4_few
 // The product for a few tokens: x as it is, or in blocks (sx not null).
 struct Mx4Few {
     const void* x;                 // [m][k] of xdt, ldx elements from row to row; or codes [m][nb * 16]

@@ -227,24 +227,30 @@ def fsdp_mx4_matmul(a, b, out=None, dtype=torch.bfloat16, stream=None):
     return out
 
 
+def _space(nbytes, device, stream):
+    """(tensor that keeps it, address, bytes) of a call's workspace."""
+    if nbytes <= 0:                              # none needed, or sizes that the call itself refuses
+        return None, None, 0
+    with _on(stream):
+        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return t, t.data_ptr(), nbytes
+
+
 def fsdp_mx4_linear(x, w, out=None, stream=None):
     """y = x W^T for x [tokens, in] and W an Mx4 [out, in]: x is quantised along
-    its features on the way (a few tokens, up to 2048 blocks of them, within the
-    one launch).  y has x's
+    its features on the way (for a few tokens within the one launch).  y has x's
     dtype unless `out` says otherwise."""
     if not isinstance(w, Mx4):
         raise TypeError("w must be an Mx4")
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != w.cols:
         raise ValueError("x must be a matrix of %d columns" % w.cols)
-    if x.shape[0] > N.MX4_FEW or x.shape[0] * w.scales.shape[1] > N.MX4_FEW_BLOCKS:
-        with _on(stream):
-            return fsdp_mx4_matmul(fsdp_mx4_quantize(x, stream=stream), w, out, x.dtype, stream)
     m, k, ldx = _matrix(x, "x")
     device = x.device
     out, ldo = _result(out, m, w.rows, x.dtype, device, stream)
     _one_device(device, w.codes, out)
-    _issue("fsdp_mx4_linear_few", device, stream, x.data_ptr(), dtype_code(x.dtype), m, k, ldx, w.codes.data_ptr(),
-           w.scales.data_ptr(), w.rows, dtype_code(out.dtype), out.data_ptr(), ldo)
+    keep, space, nbytes = _space(N.lib().fsdp_mx4_linear_workspace(m, k), device, stream)
+    _issue("fsdp_mx4_linear", device, stream, x.data_ptr(), dtype_code(x.dtype), m, k, ldx, w.codes.data_ptr(),
+           w.scales.data_ptr(), w.rows, dtype_code(out.dtype), out.data_ptr(), ldo, space, nbytes)
     return out
 
 
@@ -253,17 +259,33 @@ def fsdp_mx4_linear_grads(dy, x, wt, dx=None, dw=None, dw_dtype=None, stream=Non
     dx = dy W (dtype of x) and dw = dy^T x (dw_dtype, else the dtype of x), each
     the product of its operands quantised along the axis that it sums over.
     wt: W quantised along its columns, an Mx4 [in, out].  dx and dw may be given
-    (dw: the weight's place in a flat gradient)."""
+    (dw: the weight's place in a flat gradient); dx=False or dw=False: not
+    wanted, and None in its place."""
     if not isinstance(wt, Mx4):
         raise TypeError("wt must be an Mx4")
     for name, t, c in (("dy", dy, wt.cols), ("x", x, wt.rows)):
         if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[1] != c:
             raise ValueError("%s must be a matrix of %d columns" % (name, c))
-    if dy.shape[0] != x.shape[0]:
-        raise ValueError("dy has %d rows, x %d" % (dy.shape[0], x.shape[0]))
-    with _on(stream):
-        q, qt = fsdp_mx4_quantize(dy, form="both", stream=stream)
-        xt = fsdp_mx4_quantize(x, form="columns", stream=stream)
-        dx = fsdp_mx4_matmul(q, wt, dx, x.dtype, stream)
-        dw = fsdp_mx4_matmul(qt, xt, dw, dw_dtype or x.dtype, stream)
-    return dx, dw
+    m, n, lddy = _matrix(dy, "dy")
+    mx, k, ldx = _matrix(x, "x")
+    if m != mx:
+        raise ValueError("dy has %d rows, x %d" % (m, mx))
+    device = dy.device
+    want_dx, want_dw = dx is not False, dw is not False
+    pdx = pdw = None
+    lddx = lddw = cdx = cdw = 0
+    _one_device(device, x, wt.codes)
+    if want_dx:
+        dx, lddx = _result(dx, m, k, x.dtype, device, stream)
+        _one_device(device, dx)
+        pdx, cdx = dx.data_ptr(), dtype_code(dx.dtype)
+    if want_dw:
+        dw, lddw = _result(dw, n, k, dw_dtype or x.dtype, device, stream)
+        _one_device(device, dw)
+        pdw, cdw = dw.data_ptr(), dtype_code(dw.dtype)
+    keep, space, nbytes = _space(N.lib().fsdp_mx4_linear_grads_workspace(m, n, k, int(want_dx), int(want_dw)), device,
+                                 stream)
+    _issue("fsdp_mx4_linear_grads", device, stream, dy.data_ptr(), dtype_code(dy.dtype), lddy, x.data_ptr(),
+           dtype_code(x.dtype), ldx, m, n, k, wt.codes.data_ptr(), wt.scales.data_ptr(), cdx, pdx, lddx, cdw, pdw,
+           lddw, space, nbytes)
+    return dx if want_dx else None, dw if want_dw else None

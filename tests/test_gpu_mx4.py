@@ -284,6 +284,19 @@ def test_linear_and_its_gradients_against_the_formula(dtype, m, n, k):
     assert dx.dtype == dtype and dw.data_ptr() == flat.t[5:].data_ptr()
     _check_product(_f64(dx), q(DY), q(W.T), dtype, "dx")
     _check_product(_f64(dw), q(DY.T), q(X.T), torch.float32, "dw")
+    wt = ss.fsdp_mx4_quantize(w, form="columns")
+    alone, none = ss.fsdp_mx4_linear_grads(dy, x, wt, dw=False)
+    assert none is None and torch.equal(alone, dx)
+    none, alone = ss.fsdp_mx4_linear_grads(dy, x, wt, dx=False, dw_dtype=torch.float32)
+    assert none is None and torch.equal(alone, dw)
+
+
+def test_gradients_of_no_tokens():
+    x, dy = torch.empty(0, 64, device="cuda"), torch.empty(0, 96, device="cuda")
+    wt = ss.fsdp_mx4_quantize(_rand((96, 64)), form="columns")
+    dx, dw = ss.fsdp_mx4_linear_grads(dy, x, wt)
+    assert dx.shape == (0, 64) and torch.equal(dw, torch.zeros(96, 64, device="cuda"))
+    assert ss.fsdp_mx4_linear(x, ss.fsdp_mx4_quantize(_rand((96, 64)))).shape == (0, 96)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)

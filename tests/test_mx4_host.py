@@ -105,22 +105,55 @@ def test_matmul_refuses():
     assert call(m=0) == N.OK and call(n=0, ldo=0) == N.OK
 
 
-def test_linear_few_refuses():
+def test_linear_refuses():
     L = N.lib()
+    ws = FAKE + (5 << 30)
 
-    def call(x=FAKE, xdt=N.BF16, m=4, k=96, ldx=96, w=FAKE + (1 << 30), sw=FAKE + (2 << 30), n=64, dt=N.F16,
-             out=FAKE + (3 << 30), ldo=64):
-        return L.fsdp_mx4_linear_few(vp(x), xdt, m, k, ldx, vp(w), vp(sw), n, dt, vp(out), ldo, None)
+    def call(x=FAKE, xdt=N.BF16, m=40, k=96, ldx=96, w=FAKE + (1 << 30), sw=FAKE + (2 << 30), n=64, dt=N.F16,
+             out=FAKE + (3 << 30), ldo=64, ws=ws, nbytes=1 << 20):
+        return L.fsdp_mx4_linear(vp(x), xdt, m, k, ldx, vp(w), vp(sw), n, dt, vp(out), ldo, vp(ws), nbytes, None)
 
     assert call(xdt=3) == N.E_DTYPE and call(dt=-1) == N.E_DTYPE
-    assert call(m=17) == N.E_SIZE and call(m=-1) == N.E_INVAL and call(k=-1) == N.E_INVAL and call(n=-1) == N.E_INVAL
+    assert call(m=-1) == N.E_INVAL and call(k=-1) == N.E_INVAL and call(n=-1) == N.E_INVAL
     assert call(ldx=95) == N.E_INVAL and call(ldo=63) == N.E_INVAL
     assert call(x=0) == N.E_INVAL and call(w=0) == N.E_INVAL and call(sw=0) == N.E_INVAL and call(out=0) == N.E_INVAL
     assert call(w=FAKE + (1 << 30) + 1) == N.E_INVAL
     assert call(k=(1 << 23) + 1, ldx=1 << 24) == N.E_SIZE
-    assert call(m=16, k=129 * 32, ldx=129 * 32) == N.E_SIZE              # 2064 blocks of x
-    assert call(out=FAKE + 700) == N.E_ALIAS and call(out=FAKE + (2 << 30) + 191) == N.E_ALIAS
+    assert call(out=FAKE + 700) == N.E_ALIAS and call(out=FAKE + (2 << 30) + 190) == N.E_ALIAS
+    assert L.fsdp_mx4_linear_workspace(40, 96) == 40 * 3 * 17 + 8
+    assert call(nbytes=40 * 3 * 17 + 7) == N.E_SIZE and call(ws=0) == N.E_INVAL and call(ws=ws + 8) == N.E_INVAL
+    assert call(ws=FAKE + 1024) == N.E_ALIAS and call(ws=FAKE + (3 << 30) + 16) == N.E_ALIAS
+    assert L.fsdp_mx4_linear_workspace(1, 8192) == 0 and L.fsdp_mx4_linear_workspace(0, 8192) == 0
+    assert L.fsdp_mx4_linear_workspace(-1, 5) == -1 and L.fsdp_mx4_linear_workspace(1 << 40, 1 << 40) == -1
     assert call(m=0) == N.OK and call(n=0, ldo=0) == N.OK
+
+
+def test_linear_grads_refuses():
+    L = N.lib()
+    G = 1 << 30
+
+    def call(dy=FAKE, dydt=N.BF16, lddy=64, x=FAKE + G, xdt=N.BF16, ldx=96, m=40, n=64, k=96, wt=FAKE + 2 * G,
+             swt=FAKE + 3 * G, dxdt=N.BF16, dx=FAKE + 4 * G, lddx=96, dwdt=N.F32, dw=FAKE + 5 * G, lddw=96,
+             ws=FAKE + 6 * G, nbytes=1 << 20):
+        return L.fsdp_mx4_linear_grads(vp(dy), dydt, lddy, vp(x), xdt, ldx, m, n, k, vp(wt), vp(swt), dxdt, vp(dx),
+                                       lddx, dwdt, vp(dw), lddw, vp(ws), nbytes, None)
+
+    assert call(dydt=5) == N.E_DTYPE and call(xdt=5) == N.E_DTYPE and call(dxdt=5) == N.E_DTYPE
+    assert call(dwdt=5) == N.E_DTYPE
+    assert call(m=-1) == N.E_INVAL and call(n=-1) == N.E_INVAL and call(k=-1) == N.E_INVAL
+    assert call(lddy=63) == N.E_INVAL and call(ldx=95) == N.E_INVAL and call(lddx=95) == N.E_INVAL
+    assert call(lddw=95) == N.E_INVAL
+    assert call(dy=0) == N.E_INVAL and call(x=0) == N.E_INVAL and call(wt=0) == N.E_INVAL and call(swt=0) == N.E_INVAL
+    assert call(wt=FAKE + 2 * G + 8) == N.E_INVAL and call(ws=0) == N.E_INVAL and call(ws=FAKE + 6 * G + 4) == N.E_INVAL
+    need = L.fsdp_mx4_linear_grads_workspace(40, 64, 96, 1, 1)
+    assert need == (40 * 2 + 64 * 2 + 96 * 2) * 17                       # each a multiple of 16 already
+    assert call(nbytes=need - 1) == N.E_SIZE
+    assert L.fsdp_mx4_linear_grads_workspace(40, 64, 96, 1, 0) == 40 * 2 * 17
+    assert L.fsdp_mx4_linear_grads_workspace(40, -64, 96, 1, 0) == -1
+    assert call(dx=FAKE + 64) == N.E_ALIAS and call(dw=FAKE + 4 * G + 64) == N.E_ALIAS
+    assert call(ws=FAKE + 5 * G + 1024) == N.E_ALIAS and call(ws=FAKE + 3 * G) == N.E_ALIAS
+    assert call(m=1 << 24, lddy=64) == N.E_SIZE                          # dw sums over more than 2^23 tokens
+    assert call(dx=0, dw=0, dy=0) == N.OK and call(k=0, ldx=0, lddx=0, lddw=0) == N.OK
 
 
 def test_binding_refuses():
