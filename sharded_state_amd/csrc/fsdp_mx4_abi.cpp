@@ -28,7 +28,7 @@ int guarded(const char* fn, F&& body) {
 int check_matrix(const char* fn, int64_t rows, int64_t cols) {
     if (rows < 0 || cols < 0) return fail(FSDP_E_INVAL, "%s: a size is negative", fn);
     // padded to whole blocks a row has fewer than cols + 32 elements
-    if (rows > 0 && cols > kMaxElems / rows - kMx4Block) return fail(FSDP_E_SIZE, "%s: the matrix is too large", fn);
+    if (rows > kMaxElems || cols > kMaxElems || (rows > 0 && cols > kMaxElems / rows - kMx4Block)) return fail(FSDP_E_SIZE, "%s: the matrix is too large", fn);
     return FSDP_OK;
 }
 

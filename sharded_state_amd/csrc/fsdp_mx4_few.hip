@@ -131,15 +131,18 @@ __global__ __launch_bounds__(64 * NW) void k_mx4_few(Mx4Few p) {
             }
         }
     };
-    while (u < runs) {
-        const int64_t v = u + NW;
-        Run next;
-        if (v < whole) fetch(next, v * kRun, std::true_type{});
-        else if (v < runs) fetch(next, v * kRun, std::false_type{});
-        if (u < whole) multiply(cur, u * kRun, std::true_type{});
-        else multiply(cur, u * kRun, std::false_type{});
-        cur = next;
-        u = v;
+    if (u < runs) {
+        for (;;) {
+            const int64_t v = u + NW;
+            Run next;
+            if (v < whole) fetch(next, v * kRun, std::true_type{});
+            else if (v < runs) fetch(next, v * kRun, std::false_type{});
+            if (u < whole) multiply(cur, u * kRun, std::true_type{});
+            else multiply(cur, u * kRun, std::false_type{});
+            if (v >= runs) break;
+            cur = next;
+            u = v;
+        }
     }
 
     if constexpr (XF != kBlocked) __syncthreads();           // the sums take x's place

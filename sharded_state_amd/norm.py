@@ -58,11 +58,14 @@ class GradNorm:
     def coef(self):
         return self._buf[12:16].view(torch.float32) if self.has_coef else None
 
-    def _args(self, max_norm):
-        """(max_norm, sumsq, norm, coef) of a call, and the workspace's address."""
+    def _issue(self, name, stream, args, max_norm, workspace=True):
+        """Issue a norm call whose outputs are this object's."""
         p = self._buf.data_ptr()
-        self.has_coef = max_norm is not None
-        return (float(max_norm) if self.has_coef else 0.0, p, p + 8, p + 12 if self.has_coef else None), p + 16
+        clips = max_norm is not None
+        args += (float(max_norm) if clips else 0.0, p, p + 8, p + 12 if clips else None)
+        _issue(name, self.device, stream, *args, *((p + 16,) if workspace else ()))
+        self.has_coef = clips
+        return self
 
 
 def _out(out, device, stream):
@@ -115,9 +118,7 @@ def fsdp_grad_norm(tensors, max_norm=None, out=None, stream=None):
     device = tensors[0].device if tensors else out.device
     _same_device(tensors)
     out = _out(out, device, stream)
-    outs, ws = out._args(max_norm)
-    _issue("fsdp_grad_norm", device, stream, ptrs, numels, dts, n, *outs, ws)
-    return out
+    return out._issue("fsdp_grad_norm", stream, (ptrs, numels, dts, n), max_norm)
 
 
 def fsdp_grad_norm_units(units, rank, fp32_reduce, max_norm=None, out=None, stream=None):
@@ -161,10 +162,8 @@ def fsdp_grad_norm_units(units, rank, fp32_reduce, max_norm=None, out=None, stre
     _same_device(tensors)
     device = tensors[0].device
     out = _out(out, device, stream)
-    outs, ws = out._args(max_norm)
-    _issue("fsdp_grad_norm_units", device, stream, table, len(units), world, int(rank), dtype_code(gdt),
-           int(bool(fp32_reduce)), *outs, ws)
-    return out
+    return out._issue("fsdp_grad_norm_units", stream, (table, len(units), world, int(rank), dtype_code(gdt),
+                                                       int(bool(fp32_reduce))), max_norm)
 
 
 def fsdp_grad_norm_combine(sumsqs, max_norm=None, out=None, stream=None):
@@ -176,9 +175,7 @@ def fsdp_grad_norm_combine(sumsqs, max_norm=None, out=None, stream=None):
         raise TypeError("sumsqs must be float64")
     device = sumsqs.device
     out = _out(out, device, stream)
-    outs, _ = out._args(max_norm)
-    _issue("fsdp_grad_norm_combine", device, stream, sumsqs.data_ptr(), sumsqs.numel(), *outs)
-    return out
+    return out._issue("fsdp_grad_norm_combine", stream, (sumsqs.data_ptr(), sumsqs.numel()), max_norm, workspace=False)
 
 
 def fsdp_clip_grads(tensors, clip, stream=None):

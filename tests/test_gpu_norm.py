@@ -169,6 +169,20 @@ def test_norm_of_units_is_that_of_the_reduce_scatter(world, rank, dtype, fp32r, 
             assert_bits_equal(np_of(h.t), np_of(w), "shard")
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_a_16_bit_average_keeps_the_sign_of_zero(dtype):
+    for world in (1, 2, 3, 4, 8):
+        S = 1032
+        grads = [torch.full((world * S,), -0.0, dtype=dtype, device="cuda") for _ in range(world)]
+        out = torch.zeros(S, dtype=dtype, device="cuda")
+        gn = ss.fsdp_grad_norm_units([dict(rank_grads=grads, grad_shard=out)], 0, False, 1.0)
+        want = oracle.grad_average([np_of(g) for g in grads], 0, S, dt_name(dtype), False)
+        got = np_of(out)
+        assert np.array_equal(got, oracle.f32_to(np.asarray(want, dtype=np.float32), dt_name(dtype))
+                              if np.asarray(want).dtype == np.float32 else want)
+        assert (got == 0x8000).all() and float(gn.norm) == 0.0 and float(gn.coef) == 1.0
+
+
 def test_units_off_the_16_byte_grid():
     S, world = 3001, 2
     held = [Guarded(world * S, torch.float16, offset=2 * (q + 1), init=_rand(world * S, torch.float16, q))
