@@ -27,7 +27,8 @@
  *    call returns and allocates no device memory.
  *  - Streams.  `stream` is a hipStream_t (NULL = the null stream).  Work is
  *    enqueued asynchronously; nothing synchronizes.  Any pointer alignment is
- *    accepted; 16-byte-aligned buffers take the wide (dwordx4) path.
+ *    accepted unless the call says otherwise; 16-byte-aligned buffers take the
+ *    wide (dwordx4) path.
  *  - Errors.  Every argument is validated on the host before anything is
  *    enqueued; on a negative status nothing was launched and
  *    fsdp_last_error() returns a message (thread-local).  Nothing throws or
