@@ -38,12 +38,12 @@ template <int F>
 static hipError_t product(const Mx4Product& p) {
     auto tiles = [&](int64_t t) { return ((p.m + t - 1) / t) * ((p.n + t - 1) / t); };
     const int64_t enough = p.cus * 5 / 8;
-    if (tiles(256) >= enough) return launch_tiles<F, 256, 256, 2, 4, 1, 2>(p);
+    if (tiles(256) >= enough) return launch_tiles<F, 256, 256, 2, 4, 2>(p);
     if (p.m <= kMx4Few && p.n <= 32 * (int64_t)p.cus)
         return launch_mx4_few(Mx4Few{p.a, p.sa, 0, p.m, p.nb * kMx4Block, 0, p.b, p.sb, p.n, p.nb, p.dt, p.out, p.ldo,
                                      p.cus, p.stream});
-    if (tiles(128) >= enough) return launch_tiles<F, 128, 128, 2, 2, 1, 4>(p);
-    return launch_tiles<F, 64, 64, 2, 2, 1, 4>(p);
+    if (tiles(128) >= enough) return launch_tiles<F, 128, 128, 2, 2, 4>(p);
+    return launch_tiles<F, 64, 64, 2, 2, 4>(p);
 }
 
 hipError_t launch_mx4_matmul(const Mx4Product& p) {

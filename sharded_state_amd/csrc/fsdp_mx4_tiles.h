@@ -28,16 +28,15 @@ __device__ __forceinline__ void tile_of(uint32_t b, uint32_t tiles_m, uint32_t t
     tn = in / rows;
 }
 
-// BM x BN results a workgroup of WM x WN x WK waves: a wave has BM / WM x BN / WN
-// results and every WK-th part of each stage's steps along k (the parts are
-// added in LDS at the end).  A stage is 8 blocks of 32 (a row's 128 bytes, one
-// cache line) of every row; NS stages are in LDS, NS - 1 of them on their way.
-template <int F, int BM, int BN, int WM, int WN, int WK, int NS>
+// BM x BN results a workgroup of WM x WN waves, BM / WM x BN / WN a wave.  A stage
+// is 8 blocks of 32 (a row's 128 bytes, one cache line) of every row; NS stages
+// are in LDS, NS - 1 of them on their way.
+template <int F, int BM, int BN, int WM, int WN, int NS>
 __device__ __forceinline__ void mx4_tile(const Mx4Product& p, uint32_t tiles_m, uint32_t tiles_n) {
     constexpr int KB = 8;
-    constexpr int kWaves = WM * WN * WK;
+    constexpr int kWaves = WM * WN;
     constexpr int FM = BM / WM / 32, FN = BN / WN / 32;     // fragments of 32 rows a wave
-    constexpr int kSteps = KB / 2 / WK;                      // steps of 64 along k a wave takes of a stage
+    constexpr int kSteps = KB / 2;                           // steps of 64 along k
     constexpr int kRow = KB * 16;                            // bytes of a row's stage
     constexpr int kLoads = (BM + BN) * KB / 64 / kWaves;     // 1 KB loads a wave a stage
     constexpr int kLoadsA = BM * KB / 64 / kWaves;
@@ -50,7 +49,6 @@ __device__ __forceinline__ void mx4_tile(const Mx4Product& p, uint32_t tiles_m, 
     constexpr int kScales = NS * kStage;                     // where the scales lie: 2 x (BM + BN) rows of 16 bytes
     static_assert(kLoadsA * 64 * kWaves == BM * KB && kLoads * 64 * kWaves == (BM + BN) * KB, "whole loads");
     static_assert(WM * WN * 32 * kOutRow <= kScales, "results pass through the stages' LDS");
-    static_assert((WK - 1) * WM * WN * FM * FN * 4096 <= kScales, "so do the partial sums");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kScales + 2 * (BM + BN) * 16];
 
     uint32_t tm, tn;
@@ -137,13 +135,13 @@ __device__ __forceinline__ void mx4_tile(const Mx4Product& p, uint32_t tiles_m, 
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{0};
 
-    const int wk = WK == 1 ? 0 : w / (WM * WN), wm = WK == 1 ? w / WN : w / WN % WM, wn = w % WN;
+    const int wm = w / WN, wn = w % WN;
     const int arow = (wm * FM * 32 + (l & 31)) * kRow, brow = (BM + wn * FN * 32 + (l & 31)) * kRow;
     const int tl = turn(l & 31);                             // fragments start at multiples of 32 rows
     const int srow = kScales + (wm * FM * 32 + (l & 31)) * 16, trow = kScales + (BM + wn * FN * 32 + (l & 31)) * 16;
-    // a lane needs the scales of its half h: bytes h and h + 2 of a dword for two steps of a wave
-    const int shift = 8 * h + (kSteps == 1 ? 16 * (wk & 1) : 0);
-    constexpr int kDwords = kSteps == 1 ? 1 : kSteps / 2;
+    // a lane needs the scales of its half h: bytes h and h + 2 of a dword for two steps
+    const int shift = 8 * h;
+    constexpr int kDwords = kSteps / 2;
 
     u32x4 scales[kRows];
     // Stage kt.  `more`: a stage is left to be loaded while this one is worked on.
@@ -165,7 +163,7 @@ __device__ __forceinline__ void mx4_tile(const Mx4Product& p, uint32_t tiles_m, 
         asm volatile("" ::: "memory");
         if (kt % 2 == 0 && kt + 2 < nk) fetch_scales(scales, kt / 2 + 1);
         const uint8_t* base = lds + kt % NS * kStage;
-        const int soff = (kt / 2 & 1) * (BM + BN) * 16 + kt % 2 * 8 + (wk * kSteps / 2) * 4;
+        const int soff = (kt / 2 & 1) * (BM + BN) * 16 + kt % 2 * 8;
         int sa[FM][kDwords], sb[FN][kDwords];
 #pragma unroll
         for (int d = 0; d < kDwords; ++d) {
@@ -181,12 +179,12 @@ __device__ __forceinline__ void mx4_tile(const Mx4Product& p, uint32_t tiles_m, 
         i32x8 a[2][FM], b[2][FN];
         auto read_a = [&](int s, int f) {
             const u32x4 v = *reinterpret_cast<const u32x4*>(base + arow + f * 32 * kRow +
-                                                            ((2 * (wk * kSteps + s) + h) ^ tl) * 16);
+                                                            ((2 * s + h) ^ tl) * 16);
             a[s & 1][f] = i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
         };
         auto read_b = [&](int s, int f) {
             const u32x4 v = *reinterpret_cast<const u32x4*>(base + brow + f * 32 * kRow +
-                                                            ((2 * (wk * kSteps + s) + h) ^ tl) * 16);
+                                                            ((2 * s + h) ^ tl) * 16);
             b[s & 1][f] = i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
         };
 #pragma unroll
@@ -233,33 +231,9 @@ __device__ __forceinline__ void mx4_tile(const Mx4Product& p, uint32_t tiles_m, 
     for (; kt < nk; ++kt) stage(kt, std::false_type{});
     __syncthreads();
 
-    if constexpr (WK > 1) {
-        // The other parts' sums, added in their order.
-        f32x16* part = reinterpret_cast<f32x16*>(lds);
-        if (wk > 0) {
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    part[(((wk - 1) * WM * WN + wm * WN + wn) * FM * FN + i * FN + j) * 64 + l] = acc[i][j];
-        }
-        __syncthreads();
-        if (wk == 0) {
-#pragma unroll
-            for (int k = 1; k < WK; ++k)
-#pragma unroll
-                for (int i = 0; i < FM; ++i)
-#pragma unroll
-                    for (int j = 0; j < FN; ++j)
-                        acc[i][j] += part[(((k - 1) * WM * WN + wm * WN + wn) * FM * FN + i * FN + j) * 64 + l];
-        }
-        __syncthreads();
-        if (wk > 0) return;
-    }
-
     // Results: each wave turns 32 rows at a time through LDS of its own, so
     // that its stores cover whole runs of a row.
-    uint8_t* mine = lds + (wm * WN + wn) * 32 * kOutRow;
+    uint8_t* mine = lds + w * 32 * kOutRow;
     constexpr int kLanes = FN * 32 * kEs / 16;               // lanes a row
     const int64_t col0 = n0 + wn * FN * 32;
 #pragma unroll
@@ -306,17 +280,17 @@ __device__ __forceinline__ void mx4_tile(const Mx4Product& p, uint32_t tiles_m, 
     }
 }
 
-template <int F, int BM, int BN, int WM, int WN, int WK, int NS>
-__global__ __launch_bounds__(64 * WM * WN * WK) void k_mx4_tiles(Mx4Product p, uint32_t tiles_m, uint32_t tiles_n) {
-    mx4_tile<F, BM, BN, WM, WN, WK, NS>(p, tiles_m, tiles_n);
+template <int F, int BM, int BN, int WM, int WN, int NS>
+__global__ __launch_bounds__(64 * WM * WN) void k_mx4_tiles(Mx4Product p, uint32_t tiles_m, uint32_t tiles_n) {
+    mx4_tile<F, BM, BN, WM, WN, NS>(p, tiles_m, tiles_n);
 }
 
-template <int F, int BM, int BN, int WM, int WN, int WK, int NS>
+template <int F, int BM, int BN, int WM, int WN, int NS>
 static hipError_t launch_tiles(const Mx4Product& p) {
     const int64_t tm = (p.m + BM - 1) / BM, tn = (p.n + BN - 1) / BN;
     // a launch holds fewer than 2^32 work items
-    if (tm * tn >= (int64_t(1) << 32) / (64 * WM * WN * WK)) return hipErrorInvalidValue;
-    launch(k_mx4_tiles<F, BM, BN, WM, WN, WK, NS>, dim3((unsigned)(tm * tn)), dim3(64 * WM * WN * WK), (hipStream_t)p.stream,
+    if (tm * tn >= (int64_t(1) << 32) / (64 * WM * WN)) return hipErrorInvalidValue;
+    launch(k_mx4_tiles<F, BM, BN, WM, WN, NS>, dim3((unsigned)(tm * tn)), dim3(64 * WM * WN), (hipStream_t)p.stream,
            p, (uint32_t)tm, (uint32_t)tn);
     return hipGetLastError();
 }

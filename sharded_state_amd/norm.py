@@ -74,6 +74,8 @@ def _out(out, device, stream):
             return GradNorm(device)
     if not isinstance(out, GradNorm):
         raise TypeError("out must be a GradNorm")
+    if out.device.type != "cuda":
+        raise ValueError("out must be on a device, got %s" % out.device)
     if out.device != device:
         raise ValueError("out is on %s, the gradients on %s" % (out.device, device))
     return out

@@ -258,6 +258,18 @@ def test_product_with_nan_blocks_and_extreme_scales(m, n, k):
     assert np.array_equal(got, _mx4_values(a) @ _mx4_values(b).T)
 
 
+@pytest.mark.parametrize("m,n,k", [(2, 40, 128), (20, 70, 160), (70, 64, 288), (200, 270, 320), (3000, 5000, 96)])
+def test_product_of_zeros_with_the_largest_scales(m, n, k):
+    """Zero codes (of both signs) give zeros whatever the scales; what overflows fp32 is infinite."""
+    a, b = _random_blocks(m, k, 11, 254, 255), _random_blocks(n, k, 12, 254, 255)
+    a.codes[::2] &= 0x88                         # zeros
+    b.codes.fill_(0x22)                          # ones
+    a.codes[1::2] = 0x22
+    got = ss.fsdp_mx4_matmul(a, b, dtype=torch.float32)
+    assert (got[::2] == 0).all()
+    assert (got[1::2] == float("inf")).all()
+
+
 def test_product_of_empty_operands():
     a, b = ss.Mx4.empty(3, 0), ss.Mx4.empty(5, 0)
     assert torch.equal(ss.fsdp_mx4_matmul(a, b, dtype=torch.float32), torch.zeros(3, 5, device="cuda"))

@@ -138,3 +138,5 @@ def test_binding_refuses():
     assert gn.coef is None and gn.sumsq.dtype == torch.float64 and gn.norm.numel() == 1
     with pytest.raises(ValueError):
         ss.fsdp_clip_grads([], gn)                                       # taken without max_norm
+    with pytest.raises(ValueError):
+        ss.fsdp_grad_norm([], out=gn)                                    # host memory
