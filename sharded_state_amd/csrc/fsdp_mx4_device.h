@@ -115,22 +115,39 @@ __device__ __forceinline__ Raw8<F> load8_raw(const char* p) {
     }
     return x;
 }
-// n elements at p where n < 8, the rest zero.
+// n elements at p where n < 8, the rest zero.  Behind the last one it is read
+// again: loads under conditions of their own wait for each other.
 template <int F>
 __device__ __forceinline__ Raw8<F> load_upto8(const char* p, int64_t n) {
     if (n >= 8) return load8_raw<F>(p);
-    Raw8<F> x;
+    Raw8<F> x{};
+    if (n <= 0) return x;
+    const int m = (int)n;
     if constexpr (F == FSDP_F32) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x.w[k] = k < n ? ((const uint32_t*)p)[k] : 0u;
-    } else {
+        for (int k = 0; k < 8; ++k) x.w[k] = ((const uint32_t*)p)[k < m ? k : m - 1];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            x.w[k] = 2 * k < n ? ((const uint16_t*)p)[2 * k] : 0u;
-            if (2 * k + 1 < n) x.w[k] |= (uint32_t)((const uint16_t*)p)[2 * k + 1] << 16;
-        }
+        for (int k = 1; k < 8; ++k) x.w[k] = k < m ? x.w[k] : 0u;
+    } else {
+        uint32_t e[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) e[k] = ((const uint16_t*)p)[k < m ? k : m - 1];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            x.w[k] = (2 * k < m ? e[2 * k] : 0u) | (2 * k + 1 < m ? e[2 * k + 1] << 16 : 0u);
     }
     return x;
+}
+
+// The n scales at p, n > 0, at most 16 of them, the rest zero.
+__device__ __forceinline__ u32x4 scales16(const uint8_t* p, int n) {
+    if (n >= 16) return *(const u32x4_any*)p;
+    uint32_t e[16], x[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 16; ++j) e[j] = p[j < n ? j : n - 1];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j / 4] |= j < n ? e[j] << (8 * (j % 4)) : 0u;
+    return u32x4{x[0], x[1], x[2], x[3]};
 }
 
 }  // namespace fsdp

@@ -64,14 +64,7 @@ __global__ __launch_bounds__(64 * NW) void k_mx4_few(Mx4Few p) {
                 if (kFull || b0 + 4 * k + q < nb) r.c[f][k] = *reinterpret_cast<const u32x4*>(wrow[f] + (b0 + 4 * k) * 16);
                 else r.c[f][k] = u32x4{0, 0, 0, 0};
             }
-            if constexpr (kFull) {
-                r.s[f] = *(const u32x4_any*)(srow[f] + b0);
-            } else {
-                r.s[f] = u32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int j = 0; j < kRun; ++j)
-                    if (b0 + j < nb) r.s[f][j / 4] |= (uint32_t)srow[f][b0 + j] << (8 * (j % 4));
-            }
+            r.s[f] = scales16(srow[f] + b0, kFull ? kRun : (int)(nb - b0));
         }
     };
     const int64_t whole = nb / kRun, runs = (nb + kRun - 1) / kRun;

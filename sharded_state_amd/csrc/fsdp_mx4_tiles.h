@@ -109,15 +109,7 @@ __device__ __forceinline__ void mx4_tile(const Mx4Product& p, uint32_t tiles_m, 
             if ((i + 1) * kThreadsWg > BM + BN && r >= BM + BN) break;
             const uint8_t* q = r < BM ? p.sa + (m0 + (r < rows_a ? r : rows_a - 1)) * nb
                                       : p.sb + (n0 + (r - BM < rows_b ? r - BM : rows_b - 1)) * nb;
-            if (b0 + 16 <= nb) {
-                s[i] = *(const u32x4_any*)(q + b0);
-            } else {
-                uint32_t x[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (b0 + j < nb) x[j / 4] |= (uint32_t)q[b0 + j] << (8 * (j % 4));
-                s[i].x = x[0]; s[i].y = x[1]; s[i].z = x[2]; s[i].w = x[3];
-            }
+            s[i] = scales16(q + b0, nb - b0);
         }
     };
     auto put_scales = [&](const u32x4 (&s)[kRows], int g) {
