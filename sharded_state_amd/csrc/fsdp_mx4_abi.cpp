@@ -75,10 +75,17 @@ int check_space(const char* fn, void* ws, int64_t have, int64_t need, std::vecto
     return FSDP_OK;
 }
 
-// Whether a linear product quantises x on the way (fsdp_mx4_few.hip): measured
-// with the quantisation as a launch of its own, us: 16 tokens, 6400 x 1600 (800
-// blocks) 7.5 against 7.0 and one launch less, 8192 x 8192 (4096) 19.0 against 15.4.
-bool linear_few(int64_t m, int64_t k) { return m <= kMx4Few && m * mx4_blocks(k) <= 2048; }
+// Whether a linear product quantises x on the way (fsdp_mx4_few.hip).  Every
+// workgroup then does, which costs m blocks for 16 of W; a launch of its own 2.4
+// us.  Up to 3 tokens it pays whatever k is (us, on the way and apart: one token,
+// 8192 x 28672 25.5 and 27.6; 3 tokens, 8192 x 8192 11.9 and 13.4, 28672 x 8192 30.7
+// and 29.4; 8 tokens 45.8 and 32.4), as far as LDS holds the blocks; for more where
+// the blocks are few (16 tokens, 1000 x 1000 (512 blocks) 4.2 and 5.2, 5120 x 1280
+// (640) 6.8 and 6.6, 6400 x 1600 (800) 7.9 and 7.2).
+bool linear_few(int64_t m, int64_t k) {
+    const int64_t blocks = m * mx4_blocks(k);
+    return (m <= 3 && blocks <= 2048) || (m <= kMx4Few && blocks <= 640);
+}
 
 }  // namespace
 

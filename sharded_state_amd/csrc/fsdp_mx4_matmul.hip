@@ -22,9 +22,10 @@
 namespace fsdp {
 
 // For up to 16 rows of A the product is a read of B, and k_mx4_few reads it with
-// more loads on their way than few tiles do, as long as it is a workgroup a CU (16
-// rows with their quantisation, us: 8192 x 28672 38.8 against 55 in tiles, 8192 x
-// 8192 15.6 against 20; but 10240 x 8192 23.6 against 20.8).
+// more loads on their way than few tiles do (16 rows, us: 8192 x 28672 28.3 against
+// 54.7 in tiles, 4096 x 4096 4.7 and 8.3, 10240 x 8192 14.3 and 18.2, 20480 x 5120
+// 16.7 and 17.3), until the tiles are many (28672 x 8192 32.1 against 28.8, 40000 x
+// 512 7.5 and 5.8).
 // Else the largest tile that gives at least 5/8 of the CUs a tile (measured, us):
 //   6400 x 1600 x 1000  256: 13.4 (175 tiles)  128: 16.9 (650)   64: 19.1
 //   3000 x 5000 x 700   256: 14.9 (240 tiles)  128: 24.6         64: 31.3
@@ -39,7 +40,7 @@ static hipError_t product(const Mx4Product& p) {
     auto tiles = [&](int64_t t) { return ((p.m + t - 1) / t) * ((p.n + t - 1) / t); };
     const int64_t enough = p.cus * 5 / 8;
     if (tiles(256) >= enough) return launch_tiles<F, 256, 256, 2, 4, 2>(p);
-    if (p.m <= kMx4Few && p.n <= 32 * (int64_t)p.cus)
+    if (p.m <= kMx4Few && p.n <= 96 * (int64_t)p.cus)
         return launch_mx4_few(Mx4Few{p.a, p.sa, 0, p.m, p.nb * kMx4Block, 0, p.b, p.sb, p.n, p.nb, p.dt, p.out, p.ldo,
                                      p.cus, p.stream});
     if (tiles(128) >= enough) return launch_tiles<F, 128, 128, 2, 2, 4>(p);

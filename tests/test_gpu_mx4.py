@@ -314,7 +314,9 @@ def test_gradients_of_no_tokens():
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 17, 33), (2, 100, 512), (1, 8200, 700), (3, 16400, 96),
                                    (16, 1280, 5000), (17, 300, 1024), (31, 8192 + 5, 160), (32, 16384 + 48, 544),
-                                   (33, 200, 96), (5, 1600, 4097), (32, 65, 9000)])
+                                   (33, 200, 96), (5, 1600, 4097), (32, 65, 9000), (1, 40, 65_536), (1, 40, 65_568),
+                                   (3, 50, 21_830), (3, 50, 21_857), (2, 33, 2050), (16, 31, 1280), (16, 4100, 1281),
+                                   (9, 24_600, 97), (1, 15, 16_000)])
 def test_linear_of_few_tokens(dtype, m, n, k):
     """Few tokens in one launch, and more: strided and unaligned x and y, and the
     same values as quantisation and product one after the other."""
