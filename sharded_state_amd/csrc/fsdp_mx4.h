@@ -22,7 +22,9 @@ struct Mx4Quant {
     uint8_t* codes_t;              // blocks along the columns, or null
     uint8_t* scales_t;
 };
-hipError_t launch_mx4_quantize(const Mx4Quant& q, void* stream);
+// With `also`, which has q's dt and as q blocks along the columns (and no others),
+// that matrix too in the same launch.
+hipError_t launch_mx4_quantize(const Mx4Quant& q, const Mx4Quant* also, void* stream);
 
 struct Mx4Shards {
     const uint8_t* codes[FSDP_MAX_WORLD];

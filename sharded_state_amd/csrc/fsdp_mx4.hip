@@ -66,16 +66,22 @@ __global__ __launch_bounds__(kThreads) void k_mx4_rows(const char* __restrict__ 
 // tiles write to a line of the transpose (64 bytes of codes, 4 of scales each)
 // meets in one L2.
 constexpr int kTile = 128;
+struct Mx4Cols {
+    Mx4Quant q;
+    uint32_t tiles_r, tiles;       // tiles down the rows, and in all
+};
+// Tile number `b` of job `j`, in the order of the launch.
 template <int F, bool ROWS>
-__global__ __launch_bounds__(kThreads) void k_mx4_cols(const char* __restrict__ src, int64_t rows, int64_t cols,
-                                                       int64_t ld, uint32_t tiles_r, uint32_t tiles,
-                                                       uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
-                                                       uint8_t* __restrict__ codes_t, uint8_t* __restrict__ scales_t) {
+__device__ __forceinline__ void cols_tile(const Mx4Cols& j, uint32_t b, uint8_t* lds) {
     constexpr int kEs = F == FSDP_F32 ? 4 : 2;
     constexpr int kPass = kThreads / (kTile / 8);            // rows a pass
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kTile * kTile * kEs];     // later the codes, 8.8 KB
-    const uint32_t x = blockIdx.x & 7, per = tiles >> 3, more = tiles & 7;
-    const uint32_t t = x * per + (x < more ? x : more) + (blockIdx.x >> 3);
+    const char* __restrict__ src = (const char*)j.q.src;
+    const int64_t rows = j.q.rows, cols = j.q.cols, ld = j.q.ld;
+    uint8_t *__restrict__ codes = j.q.codes, *__restrict__ scales = j.q.scales;
+    uint8_t *__restrict__ codes_t = j.q.codes_t, *__restrict__ scales_t = j.q.scales_t;
+    const uint32_t tiles_r = j.tiles_r, tiles = j.tiles;
+    const uint32_t x = b & 7, per = tiles >> 3, more = tiles & 7;
+    const uint32_t t = x * per + (x < more ? x : more) + (b >> 3);
     // Tiles go down the rows; with the row form too, kPair columns of them together,
     // so that a row's stores of neighbouring tiles meet in the L2 (bf16 8192 x 10240:
     // 61.6 us, one column at a time 63.3; fp32 110 and 115).  The transpose alone
@@ -159,6 +165,20 @@ __global__ __launch_bounds__(kThreads) void k_mx4_cols(const char* __restrict__ 
     }
 }
 
+// With PAIR a second matrix's columns in the same launch, from the next multiple
+// of 8 workgroups on (a linear layer's gradients take both operands' at once).
+template <int F, bool ROWS, bool PAIR>
+__global__ __launch_bounds__(kThreads) void k_mx4_cols(Mx4Cols a, Mx4Cols also) {
+    // the tile as it is, later its codes (8.8 KB)
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kTile * kTile * (F == FSDP_F32 ? 4 : 2)];
+    const uint32_t first = (a.tiles + 7) & ~7u;
+    if (!PAIR || blockIdx.x < first) {
+        if (!PAIR || blockIdx.x < a.tiles) cols_tile<F, ROWS>(a, blockIdx.x, lds);
+    } else {
+        cols_tile<F, false>(also, blockIdx.x - first, lds);
+    }
+}
+
 // The all-gather of quantised shards into the full buffer of format F: a lane
 // makes two 16-byte vectors of a 16-bit format (8 elements each) or four of
 // fp32 (4 elements each), loads first.  With WIDE every slot starts on the 16-byte grid and a wave's
@@ -236,19 +256,26 @@ static unsigned capped(int64_t want) {
     return (unsigned)(want < 1 ? 1 : (want < cap ? want : cap));
 }
 
+constexpr int64_t kMaxTiles = (1 << 23) - 8;      // two jobs of a launch hold fewer than 2^32 work items
+
+static bool cols_job(const Mx4Quant& q, Mx4Cols& j) {
+    const int64_t tr = (q.rows + kTile - 1) / kTile, tc = (q.cols + kTile - 1) / kTile;
+    if (tr > kMaxTiles / tc) return false;
+    j = Mx4Cols{q, (uint32_t)tr, (uint32_t)(tr * tc)};
+    return true;
+}
+
 template <int F>
-static hipError_t quantize(const Mx4Quant& q, hipStream_t st) {
+static hipError_t quantize(const Mx4Quant& q, const Mx4Quant* also, hipStream_t st) {
     const char* src = (const char*)q.src;
     if (q.codes_t) {
-        const int64_t tr = (q.rows + kTile - 1) / kTile, tc = (q.cols + kTile - 1) / kTile;
-        if (tr > ((1 << 24) - 1) / tc) return hipErrorInvalidValue;   // a launch holds fewer than 2^32 work items
-        const dim3 g((unsigned)(tr * tc)), th(kThreads);
-        if (q.codes)
-            launch(k_mx4_cols<F, true>, g, th, st, src, q.rows, q.cols, q.ld, (uint32_t)tr, (uint32_t)(tr * tc),
-                   q.codes, q.scales, q.codes_t, q.scales_t);
-        else
-            launch(k_mx4_cols<F, false>, g, th, st, src, q.rows, q.cols, q.ld, (uint32_t)tr, (uint32_t)(tr * tc),
-                   q.codes, q.scales, q.codes_t, q.scales_t);
+        Mx4Cols a, b{};
+        if (!cols_job(q, a) || (also && !cols_job(*also, b))) return hipErrorInvalidValue;
+        const dim3 g(also ? ((a.tiles + 7) & ~7u) + b.tiles : a.tiles), th(kThreads);
+        if (q.codes && also) launch(k_mx4_cols<F, true, true>, g, th, st, a, b);
+        else if (q.codes) launch(k_mx4_cols<F, true, false>, g, th, st, a, b);
+        else if (also) launch(k_mx4_cols<F, false, true>, g, th, st, a, b);
+        else launch(k_mx4_cols<F, false, false>, g, th, st, a, b);
         return hipGetLastError();
     }
     int64_t rows = q.rows, cols = q.cols;
@@ -262,11 +289,11 @@ static hipError_t quantize(const Mx4Quant& q, hipStream_t st) {
     return hipGetLastError();
 }
 
-hipError_t launch_mx4_quantize(const Mx4Quant& q, void* stream) {
+hipError_t launch_mx4_quantize(const Mx4Quant& q, const Mx4Quant* also, void* stream) {
     hipStream_t st = (hipStream_t)stream;
-    if (q.dt == FSDP_F32) return quantize<FSDP_F32>(q, st);
-    if (q.dt == FSDP_F16) return quantize<FSDP_F16>(q, st);
-    return quantize<FSDP_BF16>(q, st);
+    if (q.dt == FSDP_F32) return quantize<FSDP_F32>(q, also, st);
+    if (q.dt == FSDP_F16) return quantize<FSDP_F16>(q, also, st);
+    return quantize<FSDP_BF16>(q, also, st);
 }
 
 template <int F>

@@ -303,6 +303,18 @@ def test_linear_and_its_gradients_against_the_formula(dtype, m, n, k):
     assert none is None and torch.equal(alone, dw)
 
 
+@pytest.mark.parametrize("m,n,k", [(3, 40, 70), (130, 300, 200), (300, 1100, 140)])
+def test_gradients_of_operands_of_two_dtypes(m, n, k):
+    """dy and x of one dtype are quantised in one launch, of two in a launch each: the same values."""
+    x, w = _rand((m, k), torch.bfloat16, 1), _rand((n, k), torch.bfloat16, 2, 0.05)
+    dy = _rand((m, n), torch.bfloat16, 3, 0.01)
+    wt = ss.fsdp_mx4_quantize(w, form="columns")
+    same = ss.fsdp_mx4_linear_grads(dy, x, wt)
+    for a, b in ((dy.float(), x), (dy, x.float()), (dy.float(), x.float())):
+        dx, dw = ss.fsdp_mx4_linear_grads(a, b, wt)
+        assert torch.equal(dx.to(torch.bfloat16), same[0]) and torch.equal(dw.to(torch.bfloat16), same[1])
+
+
 def test_gradients_of_no_tokens():
     x, dy = torch.empty(0, 64, device="cuda"), torch.empty(0, 96, device="cuda")
     wt = ss.fsdp_mx4_quantize(_rand((96, 64)), form="columns")
