@@ -2,14 +2,13 @@
 // scale of a block, its codes, and loads at any address.  Not installed.
 #pragma once
 
-#include "fsdp_device.h"
+#include "fsdp_any.h"
 #include "fsdp_mx4.h"
 
 #pragma clang fp contract(off)
 
 namespace fsdp {
 
-typedef u32x4 u32x4_any __attribute__((aligned(1)));
 typedef u32x2 u32x2_any __attribute__((aligned(1)));
 typedef uint32_t u32_any __attribute__((aligned(1)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));

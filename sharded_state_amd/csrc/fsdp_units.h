@@ -15,7 +15,7 @@
 // 指南" (zskr.cn), "工作原理" and "限制与兼容性说明".
 #pragma once
 
-#include "fsdp_device.h"
+#include "fsdp_any.h"
 #include "fsdp_optim.h"
 
 #pragma clang fp contract(off)
@@ -119,6 +119,39 @@ __device__ __forceinline__ void unit_vec(const UnitBatch<NW>& B, int u, int64_t 
     if (out2) store8x<CF, kG>(out2, vi, pp);
 }
 
+// The clipped step of vector vi of a unit with a buffer off the 16-byte grid: 8
+// consecutive elements of every stream, through 16-byte accesses at any address.
+// Element by element, as the step without clipping has such units, and so, us: N = 2
+// bf16, shards of 15,000,001 with the all-gather 217.7 and 99.8 (its bytes at the
+// copy rate 78.5), N = 8 bf16 5,000,001 174.7 and 71.2 (53.8), N = 6 fp16 1,400,001
+// 44.4 and 24.4 (12.5), N = 4 fp16 9,999,999 without the all-gather 70.9 and 72.7.
+template <class OPT, int NW, int GF, bool FP32R, int CF, bool GATHER, int SF>
+__device__ __forceinline__ void unit_any(const UnitBatch<NW>& B, int u, int64_t vi, const ReduceScalars& rs,
+                                         const OPT& op, float clip) {
+    constexpr int kS = SF == FSDP_F32 ? 32 : 16, kC = CF == FSDP_F32 ? 32 : 16;     // bytes of a vector
+    char* p = (char*)B.p[u] + vi * kS;
+    char* m = (char*)B.m[u] + vi * kS;
+    char* v = (char*)B.v[u] + vi * kS;
+    float acc[8], pp[8], mm[8] = {}, vv[8] = {};
+    load8_any<SF>(p, pp);
+    if constexpr (OPT::kStates >= 1) load8_any<SF>(m, mm);
+    if constexpr (OPT::kStates >= 2) load8_any<SF>(v, vv);
+    reduce8_any<NW, GF, FP32R>(UnitGrads<NW>{B, u}, B.world, vi, acc);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) op(clipped<OPT>(finish<NW, GF, FP32R>(acc[k], rs), clip), pp[k], mm[k], vv[k]);
+    store8_any<SF>(p, pp);
+    if constexpr (OPT::kStates >= 1) store8_any<SF>(m, mm);
+    if constexpr (OPT::kStates >= 2) store8_any<SF>(v, vv);
+    if (B.out[u]) store8_any<CF>((char*)B.out[u] + vi * kC, pp);
+    if (B.out2[u]) store8_any<CF>((char*)B.out2[u] + vi * kC, pp);
+    if constexpr (GATHER) {
+        for (int j = 0; j < B.npeers; ++j)
+#pragma unroll
+            for (int w = 0; w < kC; w += 16)
+                *(u32x4_any*)((char*)B.pdst[u][j] + vi * kC + w) = ld_any<true>((const char*)B.psrc[u][j] + vi * kC + w);
+    }
+}
+
 // Element i of unit u, one lane (the tail past the last full vector, or every
 // element of a unit whose buffers are not 16-byte aligned).
 template <class OPT, int NW, int GF, bool FP32R, int CF, bool GATHER, int SF>
@@ -177,11 +210,16 @@ __global__ __launch_bounds__(kThreads) void k_units(UnitBatch<NW> B, ReduceScala
     }
     const int u = lo;
     const int64_t j = tile - B.tile_begin[u];
-    const int64_t nvec = B.nvec[u];
+    // the clipped step's table: bit 0 for a unit off the 16-byte grid (whole groups
+    // leave the low bits free)
+    const int64_t nvec = kClips<OPT> ? B.nvec[u] & ~int64_t(1) : B.nvec[u];
     const int64_t tv = (nvec + kThreads - 1) / kThreads;
     if (j < tv) {
         const int64_t vi = j * kThreads + threadIdx.x;
-        if (vi < nvec) unit_vec<OPT, NW, GF, FP32R, CF, GATHER, SF>(B, u, vi, rs, op, c);
+        if (vi < nvec) {
+            if (kClips<OPT> && (B.nvec[u] & 1)) unit_any<OPT, NW, GF, FP32R, CF, GATHER, SF>(B, u, vi, rs, op, c);
+            else unit_vec<OPT, NW, GF, FP32R, CF, GATHER, SF>(B, u, vi, rs, op, c);
+        }
     } else {
         const int64_t i = nvec * 8 + (j - tv) * kThreads + threadIdx.x;
         if (i < B.S[u]) unit_elem<OPT, NW, GF, FP32R, CF, GATHER, SF>(B, u, i, rs, op, c);
@@ -288,8 +326,9 @@ static hipError_t units_all(const UnitArgs* units, int n, const UnitLaunch& L, c
             if (c > 0 && packed + a.S > kLaunchShardElems) break;   // as units_in_launch
             packed += a.S;
             B.tile_begin[c] = tiles;
-            const int64_t nvec = a.nvec & ~int64_t(63);   // whole groups; the rest joins the tail
-            B.nvec[c] = nvec;
+            const bool any = kClips<OPT> && a.nvec == 0;
+            const int64_t nvec = (any ? a.S / 8 : a.nvec) & ~int64_t(63);   // whole groups; the rest joins the tail
+            B.nvec[c] = nvec | (any ? 1 : 0);
             B.S[c] = a.S;
             B.p[c] = a.p;
             B.m[c] = a.m;

@@ -260,6 +260,45 @@ def test_a_coefficient_of_one_is_the_plain_step(hp):
             assert_bits_equal(np_of(y[key]), np_of(x[key]), key)
 
 
+@pytest.mark.parametrize("offset", [1, 3])
+@pytest.mark.parametrize("world,rank,dtype,fp32r,cdt,sdt,gather,hp", [
+    (1, 0, torch.float16, True, torch.float16, torch.float32, True, ss.AdamWHP(step=2)),
+    (2, 1, torch.bfloat16, True, torch.float32, torch.float32, True, ss.AdamWHP(step=2)),
+    (3, 2, torch.float32, True, torch.bfloat16, torch.float32, True, ss.OptimHP.adadelta()),
+    (4, 0, torch.float16, False, torch.float16, torch.float32, False, ss.OptimHP.sgd()),
+    (6, 5, torch.bfloat16, False, torch.bfloat16, torch.float32, True, ss.OptimHP.sgd(momentum=0.9)),
+    (8, 3, torch.bfloat16, True, torch.float16, torch.float32, True, ss.OptimHP.adamax()),
+    (2, 0, torch.bfloat16, False, torch.bfloat16, torch.bfloat16, True, ss.AdamWHP(step=2)),
+    (5, 1, torch.float16, False, torch.float16, torch.float16, True, ss.AdamWHP(step=2)),
+])
+def test_clipped_step_off_the_16_byte_grid(world, rank, dtype, fp32r, cdt, sdt, gather, hp, offset):
+    """Units with buffers at odd offsets, beside one on the grid: a coefficient of 1
+    gives the plain step's bits, in those places and nowhere else."""
+    print("case", world, dtype, fp32r, cdt, sdt, gather, offset, flush=True)
+    sizes = [511, 5003, 70_001, 4096]
+
+    def make():
+        units, guards = _step_units(world, rank, dtype, cdt, sizes, gather, sdt=sdt), []
+        for u in units[:3]:
+            for key in ("master", "exp_avg", "exp_avg_sq", "full", "compute_shard"):
+                if u.get(key) is not None:
+                    t = u[key]
+                    g = Guarded(t.numel(), t.dtype, offset=offset * t.element_size(), init=t)
+                    guards.append(g)
+                    u[key] = g.t
+        return units, guards
+
+    (a, ga), (b, gb) = make(), make()
+    ss.fsdp_step_units(a, rank, fp32r, hp)
+    ss.fsdp_step_units(b, rank, fp32r, hp, clip=torch.ones(1, device="cuda"))
+    for g in ga + gb:
+        g.check("a buffer")
+    for x, y in zip(a, b):
+        for key in ("master", "exp_avg", "exp_avg_sq", "full", "compute_shard"):
+            if x.get(key) is not None:
+                assert_bits_equal(np_of(y[key]), np_of(x[key]), key)
+
+
 def test_clipped_step_with_16_bit_state():
     a, b = (_step_units(2, 1, torch.bfloat16, torch.bfloat16, [6000], True, sdt=torch.bfloat16) for _ in range(2))
     coef = torch.tensor([0.5], device="cuda")
