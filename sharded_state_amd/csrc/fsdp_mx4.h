@@ -42,6 +42,7 @@ struct Mx4Product {
     void* stream;
 };
 hipError_t launch_mx4_matmul(const Mx4Product& p);
+hipError_t launch_mx4_two(const Mx4Product& a, const Mx4Product& b);   // both, in one launch where neither has few rows
 
 constexpr int kMx4Few = 16;                              // most tokens of launch_mx4_few
 // The product for a few tokens: x as it is, or in blocks (sx not null).

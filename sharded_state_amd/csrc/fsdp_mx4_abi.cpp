@@ -323,11 +323,11 @@ int fsdp_mx4_linear_grads(const void* dy, fsdp_dtype dy_dt, int64_t lddy, const 
         const bool once = want_dw && m > 0 && n > 0 && dy_dt == x_dt;
         if (m > 0 && n > 0) e = launch_mx4_quantize(of_dy, once ? &of_x : nullptr, stream);
         if (e == hipSuccess && want_dw && m > 0 && !once) e = launch_mx4_quantize(of_x, nullptr, stream);
-        if (e == hipSuccess && want_dx)
-            e = launch_mx4_matmul(Mx4Product{q, sq, (const uint8_t*)wt_codes, (const uint8_t*)wt_scales, m, k, nbn,
-                                             (int)dx_dt, dx, dxr.ld, cus, stream});
-        if (e == hipSuccess && want_dw)
-            e = launch_mx4_matmul(Mx4Product{qt, st, xt, sx, n, k, nbm, (int)dw_dt, dw, dwr.ld, cus, stream});
+        const Mx4Product of_dx{q, sq, (const uint8_t*)wt_codes, (const uint8_t*)wt_scales, m, k, nbn, (int)dx_dt, dx,
+                               dxr.ld, cus, stream};
+        const Mx4Product of_dw{qt, st, xt, sx, n, k, nbm, (int)dw_dt, dw, dwr.ld, cus, stream};
+        if (e == hipSuccess && want_dx && want_dw) e = launch_mx4_two(of_dx, of_dw);
+        else if (e == hipSuccess) e = launch_mx4_matmul(want_dx ? of_dx : of_dw);
         if (e != hipSuccess) return hip_fail(e, "linear launch");
         return ok();
     });

@@ -35,22 +35,57 @@ namespace fsdp {
 //   256 x 5120 x 5120   256: 30.9 (20 tiles)   128: 15.4 (80)    64: 12.4 (320)
 // The two smaller ones keep 4 stages in LDS (128 x 128 with 2: 31.5 us instead
 // of 25.5 at 512 x 8192 x 8192): with few tiles a CU the loads' latency counts.
+static int64_t tiles(const Mx4Product& p, int64_t t) { return ((p.m + t - 1) / t) * ((p.n + t - 1) / t); }
+
+// The side of a product's tiles; 16 for k_mx4_few.
+static int side(const Mx4Product& p) {
+    const int64_t enough = p.cus * 5 / 8;
+    if (tiles(p, 256) >= enough) return 256;
+    if (p.m <= kMx4Few && p.n <= 96 * (int64_t)p.cus) return 16;
+    return tiles(p, 128) >= enough ? 128 : 64;
+}
+
 template <int F>
 static hipError_t product(const Mx4Product& p) {
-    auto tiles = [&](int64_t t) { return ((p.m + t - 1) / t) * ((p.n + t - 1) / t); };
-    const int64_t enough = p.cus * 5 / 8;
-    if (tiles(256) >= enough) return launch_tiles<F, 256, 256, 2, 4, 2>(p);
-    if (p.m <= kMx4Few && p.n <= 96 * (int64_t)p.cus)
+    switch (side(p)) {
+    case 256: return launch_tiles<F, 256, 256, 2, 4, 2>(p);
+    case 128: return launch_tiles<F, 128, 128, 2, 2, 4>(p);
+    case 64: return launch_tiles<F, 64, 64, 2, 2, 4>(p);
+    default:
         return launch_mx4_few(Mx4Few{p.a, p.sa, 0, p.m, p.nb * kMx4Block, 0, p.b, p.sb, p.n, p.nb, p.dt, p.out, p.ldo,
                                      p.cus, p.stream});
-    if (tiles(128) >= enough) return launch_tiles<F, 128, 128, 2, 2, 4>(p);
-    return launch_tiles<F, 64, 64, 2, 2, 4>(p);
+    }
 }
 
 hipError_t launch_mx4_matmul(const Mx4Product& p) {
     if (p.dt == FSDP_F32) return product<FSDP_F32>(p);
     if (p.dt == FSDP_F16) return product<FSDP_F16>(p);
     return product<FSDP_BF16>(p);
+}
+
+// Two products share a launch, the one with the longer sum first: the end of one
+// is then the beginning of the other, and a launch boundary costs about 5 us.
+// Tiles by their number together, but the largest only where each product has
+// half of what is enough: a few long ones would outlast all others (us, apart and
+// together by side; m x n x k of a layer's gradients, dx m x k and dw n x k):
+//   64 x 1024 x 1024    7.4   64: 4.6    128: 6.4    256: 9.7
+//   512 x 5120 x 1280   21.4  64: 15.5   128: 16.9   256: 35.9
+//   1000 x 6400 x 1600  34.2  64: 34.5   128: 28.6   256: 47.3 (28 + 175 tiles)
+//   2048 x 5120 x 1280  37.1  64: 37.2   128: 28.5   256: 37.0 (40 + 100)
+//   1500 x 1500 x 6000  54.4  64: 53.8   128: 44.3   256: 38.7 (144 + 144)
+//   100 x 12000 x 3000  52.3  64: 49.9   128: 45.7   256: 86.9 (12 + 564)
+//   4096 x 4096 x 4096  83.7  64: 152.7  128: 106.1  256: 78.8 (256 + 256)
+//   128 x 8192 x 8192   80.9  64: 101.3  128: 82.9   256: 102.9 (32 + 1024)
+hipError_t launch_mx4_two(const Mx4Product& a, const Mx4Product& b) {
+    if (side(a) == 16 || side(b) == 16) {
+        hipError_t e = launch_mx4_matmul(a);
+        return e == hipSuccess ? launch_mx4_matmul(b) : e;
+    }
+    const Mx4Product &x = a.nb >= b.nb ? a : b, &y = a.nb >= b.nb ? b : a;
+    const int64_t enough = a.cus * 5 / 8, ta = tiles(a, 256), tb = tiles(b, 256);
+    if (ta + tb >= enough && ta >= enough / 2 && tb >= enough / 2) return launch_two<256, 256, 2, 4, 2>(x, y);
+    if (tiles(a, 128) + tiles(b, 128) >= enough) return launch_two<128, 128, 2, 2, 4>(x, y);
+    return launch_two<64, 64, 2, 2, 4>(x, y);
 }
 
 }  // namespace fsdp

@@ -13,8 +13,9 @@ namespace fsdp {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr int kFp4 = 4;     // the instruction's code for 4-bit elements
+constexpr int kAnyFormat = -1;   // the results' format is p.dt
 
-// Where the tile that workgroup `b` of `tiles` takes lies.  Workgroups go to
+// Where the tile that workgroup `b` of a product takes lies.  Workgroups go to
 // the 8 XCDs in turn, each with an L2 of its own: XCD x takes one run of
 // consecutive tiles, and a run walks groups of 4 tile rows column by column,
 // so the 32 tiles that an XCD works on at a time share 4 panels of A and 8 of B.
@@ -32,7 +33,7 @@ __device__ __forceinline__ void tile_of(uint32_t b, uint32_t tiles_m, uint32_t t
 // is 8 blocks of 32 (a row's 128 bytes, one cache line) of every row; NS stages
 // are in LDS, NS - 1 of them on their way.
 template <int F, int BM, int BN, int WM, int WN, int NS>
-__device__ __forceinline__ void mx4_tile(const Mx4Product& p, uint32_t tiles_m, uint32_t tiles_n) {
+__device__ __forceinline__ void mx4_tile(const Mx4Product& p, uint32_t tiles_m, uint32_t tiles_n, uint32_t block) {
     constexpr int KB = 8;
     constexpr int kWaves = WM * WN;
     constexpr int FM = BM / WM / 32, FN = BN / WN / 32;     // fragments of 32 rows a wave
@@ -42,8 +43,7 @@ __device__ __forceinline__ void mx4_tile(const Mx4Product& p, uint32_t tiles_m, 
     constexpr int kLoadsA = BM * KB / 64 / kWaves;
     constexpr int kStep = kWaves * 64 / KB;                  // rows from one load of a wave to its next
     constexpr int kStage = (BM + BN) * kRow;
-    constexpr int kEs = F == FSDP_F32 ? 4 : 2;
-    constexpr int kOutRow = FN * 32 * kEs + 16;              // a result row in LDS, 16 bytes of padding
+    constexpr int kOutRow = FN * 32 * (F == FSDP_F32 || F == kAnyFormat ? 4 : 2) + 16;   // a result row in LDS, padded
     constexpr int kThreadsWg = 64 * kWaves;
     constexpr int kRows = (BM + BN + kThreadsWg - 1) / kThreadsWg;
     constexpr int kScales = NS * kStage;                     // where the scales lie: 2 x (BM + BN) rows of 16 bytes
@@ -52,7 +52,7 @@ __device__ __forceinline__ void mx4_tile(const Mx4Product& p, uint32_t tiles_m, 
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kScales + 2 * (BM + BN) * 16];
 
     uint32_t tm, tn;
-    tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    tile_of(block, tiles_m, tiles_n, tm, tn);
     const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
     const int rows_a = (int)(p.m - m0 < BM ? p.m - m0 : BM), rows_b = (int)(p.n - n0 < BN ? p.n - n0 : BN);
     const int l = threadIdx.x & 63, h = l >> 5;
@@ -226,55 +226,84 @@ __device__ __forceinline__ void mx4_tile(const Mx4Product& p, uint32_t tiles_m, 
     // Results: each wave turns 32 rows at a time through LDS of its own, so
     // that its stores cover whole runs of a row.
     uint8_t* mine = lds + w * 32 * kOutRow;
-    constexpr int kLanes = FN * 32 * kEs / 16;               // lanes a row
     const int64_t col0 = n0 + wn * FN * 32;
+    auto put = [&](auto format) {
+        constexpr int kF = decltype(format)::value, kEs = kF == FSDP_F32 ? 4 : 2;
+        constexpr int kLanes = FN * 32 * kEs / 16;           // lanes a row
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
+        for (int i = 0; i < FM; ++i) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
+            for (int j = 0; j < FN; ++j)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint8_t* o = mine + (l & 31) * kOutRow + (j * 32 + q * 8 + h * 4) * kEs;
-                if constexpr (F == FSDP_F32) {
-                    u32x4 v;
-                    v.x = __float_as_uint(acc[i][j][4 * q]); v.y = __float_as_uint(acc[i][j][4 * q + 1]);
-                    v.z = __float_as_uint(acc[i][j][4 * q + 2]); v.w = __float_as_uint(acc[i][j][4 * q + 3]);
-                    *reinterpret_cast<u32x4*>(o) = v;
-                } else {
-                    u32x2 v;
-                    v.x = from_f32<F>(acc[i][j][4 * q]) | (from_f32<F>(acc[i][j][4 * q + 1]) << 16);
-                    v.y = from_f32<F>(acc[i][j][4 * q + 2]) | (from_f32<F>(acc[i][j][4 * q + 3]) << 16);
-                    *reinterpret_cast<u32x2*>(o) = v;
+                for (int q = 0; q < 4; ++q) {
+                    uint8_t* o = mine + (l & 31) * kOutRow + (j * 32 + q * 8 + h * 4) * kEs;
+                    if constexpr (kF == FSDP_F32) {
+                        u32x4 v;
+                        v.x = __float_as_uint(acc[i][j][4 * q]); v.y = __float_as_uint(acc[i][j][4 * q + 1]);
+                        v.z = __float_as_uint(acc[i][j][4 * q + 2]); v.w = __float_as_uint(acc[i][j][4 * q + 3]);
+                        *reinterpret_cast<u32x4*>(o) = v;
+                    } else {
+                        u32x2 v;
+                        v.x = from_f32<kF>(acc[i][j][4 * q]) | (from_f32<kF>(acc[i][j][4 * q + 1]) << 16);
+                        v.y = from_f32<kF>(acc[i][j][4 * q + 2]) | (from_f32<kF>(acc[i][j][4 * q + 3]) << 16);
+                        *reinterpret_cast<u32x2*>(o) = v;
+                    }
+                }
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int t = 0; t < 32 * kLanes / 64; ++t) {
+                const int r = (t * 64 + l) / kLanes, c = (t * 64 + l) % kLanes * (16 / kEs);
+                const u32x4 v = *reinterpret_cast<const u32x4*>(mine + r * kOutRow + c * kEs);
+                const int64_t row = m0 + (wm * FM + i) * 32 + r, col = col0 + c;
+                if (row < p.m && col < p.n) {
+                    char* o = (char*)p.out + (row * p.ldo + col) * kEs;
+                    if (col + 16 / kEs <= p.n) {
+                        *(u32x4_any*)o = v;
+                    } else {
+                        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < 16 / kEs; ++e)
+                            if (col + e < p.n) {
+                                if constexpr (kF == FSDP_F32) ((uint32_t*)o)[e] = x[e];
+                                else ((uint16_t*)o)[e] = (uint16_t)(x[e / 2] >> (16 * (e & 1)));
+                            }
+                    }
                 }
             }
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int t = 0; t < 32 * kLanes / 64; ++t) {
-            const int r = (t * 64 + l) / kLanes, c = (t * 64 + l) % kLanes * (16 / kEs);
-            const u32x4 v = *reinterpret_cast<const u32x4*>(mine + r * kOutRow + c * kEs);
-            const int64_t row = m0 + (wm * FM + i) * 32 + r, col = col0 + c;
-            if (row < p.m && col < p.n) {
-                char* o = (char*)p.out + (row * p.ldo + col) * kEs;
-                if (col + 16 / kEs <= p.n) {
-                    *(u32x4_any*)o = v;
-                } else {
-                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int e = 0; e < 16 / kEs; ++e)
-                        if (col + e < p.n) {
-                            if constexpr (F == FSDP_F32) ((uint32_t*)o)[e] = x[e];
-                            else ((uint16_t*)o)[e] = (uint16_t)(x[e / 2] >> (16 * (e & 1)));
-                        }
-                }
-            }
+            __builtin_amdgcn_wave_barrier();
         }
-        __builtin_amdgcn_wave_barrier();
-    }
+    };
+    if constexpr (F != kAnyFormat) put(std::integral_constant<int, F>{});
+    else if (p.dt == FSDP_F32) put(std::integral_constant<int, FSDP_F32>{});
+    else if (p.dt == FSDP_F16) put(std::integral_constant<int, FSDP_F16>{});
+    else put(std::integral_constant<int, FSDP_BF16>{});
 }
 
 template <int F, int BM, int BN, int WM, int WN, int NS>
 __global__ __launch_bounds__(64 * WM * WN) void k_mx4_tiles(Mx4Product p, uint32_t tiles_m, uint32_t tiles_n) {
-    mx4_tile<F, BM, BN, WM, WN, NS>(p, tiles_m, tiles_n);
+    mx4_tile<F, BM, BN, WM, WN, NS>(p, tiles_m, tiles_n, blockIdx.x);
+}
+
+// Two products in one launch, the second from workgroup `first` on (a multiple of
+// 8, so that its tiles too go to the XCDs in turn).
+template <int BM, int BN, int WM, int WN, int NS>
+__global__ __launch_bounds__(64 * WM * WN) void k_mx4_two(Mx4Product a, Mx4Product b, uint32_t first, uint32_t am,
+                                                          uint32_t an, uint32_t bm, uint32_t bn) {
+    const bool second = blockIdx.x >= first;
+    if (!second && blockIdx.x >= am * an) return;
+    Mx4Product p;
+    p.a = second ? b.a : a.a;
+    p.sa = second ? b.sa : a.sa;
+    p.b = second ? b.b : a.b;
+    p.sb = second ? b.sb : a.sb;
+    p.m = second ? b.m : a.m;
+    p.n = second ? b.n : a.n;
+    p.nb = second ? b.nb : a.nb;
+    p.dt = second ? b.dt : a.dt;
+    p.out = second ? b.out : a.out;
+    p.ldo = second ? b.ldo : a.ldo;
+    mx4_tile<kAnyFormat, BM, BN, WM, WN, NS>(p, second ? bm : am, second ? bn : an,
+                                             second ? blockIdx.x - first : blockIdx.x);
 }
 
 template <int F, int BM, int BN, int WM, int WN, int NS>
@@ -284,6 +313,16 @@ static hipError_t launch_tiles(const Mx4Product& p) {
     if (tm * tn >= (int64_t(1) << 32) / (64 * WM * WN)) return hipErrorInvalidValue;
     launch(k_mx4_tiles<F, BM, BN, WM, WN, NS>, dim3((unsigned)(tm * tn)), dim3(64 * WM * WN), (hipStream_t)p.stream,
            p, (uint32_t)tm, (uint32_t)tn);
+    return hipGetLastError();
+}
+
+template <int BM, int BN, int WM, int WN, int NS>
+static hipError_t launch_two(const Mx4Product& a, const Mx4Product& b) {
+    const int64_t am = (a.m + BM - 1) / BM, an = (a.n + BN - 1) / BN, bm = (b.m + BM - 1) / BM, bn = (b.n + BN - 1) / BN;
+    const int64_t first = (am * an + 7) / 8 * 8;
+    if (first + bm * bn >= (int64_t(1) << 32) / (64 * WM * WN)) return hipErrorInvalidValue;
+    launch(k_mx4_two<BM, BN, WM, WN, NS>, dim3((unsigned)(first + bm * bn)), dim3(64 * WM * WN), (hipStream_t)a.stream,
+           a, b, (uint32_t)first, (uint32_t)am, (uint32_t)an, (uint32_t)bm, (uint32_t)bn);
     return hipGetLastError();
 }
 

@@ -303,13 +303,22 @@ def test_linear_and_its_gradients_against_the_formula(dtype, m, n, k):
     assert none is None and torch.equal(alone, dw)
 
 
-@pytest.mark.parametrize("m,n,k", [(3, 40, 70), (130, 300, 200), (300, 1100, 140)])
-def test_gradients_of_operands_of_two_dtypes(m, n, k):
-    """dy and x of one dtype are quantised in one launch, of two in a launch each: the same values."""
+@pytest.mark.parametrize("m,n,k", [(3, 40, 70), (17, 1000, 33), (130, 300, 200), (300, 1100, 140), (512, 1100, 1700),
+                                   (2100, 2110, 2600)])
+def test_gradients_together_and_alone(m, n, k):
+    """Both products in a launch give what each gives alone, and dy and x of one
+    dtype, quantised in one launch, what they give in two dtypes: each element's sum
+    runs in one order whatever the tiles."""
+    print("case", m, n, k, flush=True)
     x, w = _rand((m, k), torch.bfloat16, 1), _rand((n, k), torch.bfloat16, 2, 0.05)
     dy = _rand((m, n), torch.bfloat16, 3, 0.01)
     wt = ss.fsdp_mx4_quantize(w, form="columns")
     same = ss.fsdp_mx4_linear_grads(dy, x, wt)
+    for out in (torch.float16, torch.float32):
+        alone = ss.fsdp_mx4_linear_grads(dy, x, wt, dx=False, dw_dtype=out)[1]
+        together = ss.fsdp_mx4_linear_grads(dy, x, wt, dw_dtype=out)[1]
+        assert together.dtype == out and torch.equal(alone, together)
+    assert torch.equal(ss.fsdp_mx4_linear_grads(dy, x, wt, dw=False)[0], same[0])
     for a, b in ((dy.float(), x), (dy, x.float()), (dy.float(), x.float())):
         dx, dw = ss.fsdp_mx4_linear_grads(a, b, wt)
         assert torch.equal(dx.to(torch.bfloat16), same[0]) and torch.equal(dw.to(torch.bfloat16), same[1])
