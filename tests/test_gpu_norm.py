@@ -96,6 +96,20 @@ def test_mixed_formats_and_the_same_bits_twice():
     assert torch.equal(a.sumsq.view(torch.int64), b.sumsq.view(torch.int64))
 
 
+def test_list_refusals():
+    good, coef = torch.ones(8, device="cuda"), torch.ones(1, device="cuda")
+    for bad, what in ((torch.ones(8), ValueError), (torch.ones(8, dtype=torch.int32, device="cuda"), TypeError),
+                      (torch.ones(8, 8, device="cuda")[:, 1], ValueError), (None, TypeError),
+                      (torch.ones(8, dtype=torch.float64, device="cuda"), TypeError)):
+        with pytest.raises(what):
+            ss.fsdp_grad_norm([good, bad])
+        with pytest.raises(what):
+            ss.fsdp_clip_grads([good, bad], coef)
+    assert (good == 1).all()
+    with pytest.raises(RuntimeError):
+        ss.fsdp_clip_grads([good, good], coef)           # the same tensor twice
+
+
 def test_extreme_values():
     """fp32 values whose squares overflow or vanish in fp32, infinities, NaN."""
     for v, n in ((3e38, 1000), (1e-30, 1000), (1e-45, 7)):

@@ -125,6 +125,11 @@ def test_step_clipped_refuses():
 def test_binding_refuses():
     with pytest.raises(ValueError):
         ss.fsdp_grad_norm([torch.zeros(4)])                              # a host tensor
+    for bad in (3.0, None, [torch.zeros(4)]):
+        with pytest.raises(TypeError):
+            ss.fsdp_grad_norm([bad])                                     # no tensor
+    with pytest.raises(ValueError):
+        ss.fsdp_grad_norm([torch.zeros(4, dtype=torch.int32)])
     with pytest.raises(ValueError):
         ss.fsdp_grad_norm([])
     with pytest.raises(ValueError):
