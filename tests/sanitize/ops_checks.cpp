@@ -101,7 +101,7 @@ static void blocks(bool device) {
             for (int form = 1; form < 4; ++form) {
                 // operands far enough apart for the sizes that pass
                 const int rc = fsdp_mx4_quantize(at(0), form % 3, r, c, c, form & 1 ? at(1024) : nullptr,
-                                                 form & 1 ? at(2048) : nullptr, form & 2 ? at(3072) : nullptr,
+                                                 form & 1 ? at(2048) : nullptr, form & 2 ? at(3000) : nullptr,
                                                  form & 2 ? at(4096) : nullptr, nullptr);
                 if (small) CHECK(planned(rc));
                 else CHECK(rc <= 0);
@@ -112,12 +112,12 @@ static void blocks(bool device) {
             for (int64_t k : sizes) {
                 const bool fits = small && k >= 0 && k <= lim && (k == 0 || (r <= lim / k && c <= lim / k));
                 if (device && fits) continue;
-                const int rc = fsdp_mx4_matmul(at(0), at(1024), at(2048), at(3072), r, c, k, 1, at(4096), c, nullptr);
+                const int rc = fsdp_mx4_matmul(at(0), at(1024), at(2048), at(3000), r, c, k, 1, at(4096), c, nullptr);
                 CHECK(fits && k <= FSDP_MX4_MAX_K ? planned(rc) : rc <= 0);
-                const int l = fsdp_mx4_linear(at(0), 2, r, k, k, at(1024), at(2048), c, 0, at(3072), c, at(4096),
+                const int l = fsdp_mx4_linear(at(0), 2, r, k, k, at(1024), at(2048), c, 0, at(3000), c, at(4096),
                                               INT64_MAX, nullptr);
                 CHECK(fits && k <= FSDP_MX4_MAX_K ? planned(l) : l <= 0);
-                const int g = fsdp_mx4_linear_grads(at(0), 2, c, at(512), 2, k, r, c, k, at(1024), at(2048), 2, at(3072),
+                const int g = fsdp_mx4_linear_grads(at(0), 2, c, at(512), 2, k, r, c, k, at(1024), at(2048), 2, at(3000),
                                                     k, 0, at(4096), k, at(8192), INT64_MAX, nullptr);
                 CHECK(g <= 0);
             }
