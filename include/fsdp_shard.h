@@ -362,7 +362,9 @@ FSDP_API int fsdp_units_in_launch(int32_t world, const int64_t* shard_numels, in
  *
  * Outputs (device; each may be NULL, not all three): sumsq_out one double
  * (what the ranks of a job add up), norm_out and coef_out one float each.
- * max_norm: finite and >= 0 (looked at only with coef_out).
+ * max_norm: finite and >= 0 (looked at only with coef_out; the largest double
+ * gives the coefficient 1 for every finite norm, for a step that reads one at
+ * every issue).  Without coef_out an earlier coefficient stays where it is.
  * workspace: device, FSDP_NORM_WORKSPACE_BYTES, 8-byte aligned; needs no
  * preparation and keeps nothing.  Calls that may run at the same time, replays
  * of two captured graphs among them, need a workspace and outputs each.

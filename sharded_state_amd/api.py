@@ -316,8 +316,9 @@ def prepare_step_units(units, rank, fp32_reduce, hp, stream=None, clip=None):
     state dtype is the dtype of the units' master tensors: float32 (fp32
     master, m, v) or bfloat16 / float16 (16-bit parameter, m, v; the parameter
     shard is the compute shard, so no compute_shard is given).  With clip the
-    call reads the coefficient from that device memory at every issue, and
-    call.hp is an OptimHP."""
+    call reads the coefficient from that device memory at every issue (1 there
+    after a norm taken into the same GradNorm without max_norm), and call.hp is an
+    OptimHP."""
     if not units:
         raise ValueError("units is empty")
     hp = _own_hp(hp)

@@ -15,9 +15,12 @@ all-reduce of one double) and takes the norm of the whole from
 
 A norm that is not finite is applied as the formula says: an infinite one gives
 coefficient 0, a NaN one gives NaN.  A loop that wants to skip such a step reads
-``norm`` before it steps.
+``norm`` before it steps.  A norm taken without max_norm leaves the coefficient
+of the largest bound in its GradNorm: 1 for every finite norm, so a prepared or
+captured step that reads it is not clipped by an earlier norm.
 """
 import ctypes
+import sys
 from array import array
 
 import torch
@@ -34,7 +37,9 @@ class GradNorm:
     the norm, the clipping coefficient and the call's workspace.
 
     sumsq  float64, 1 element;  norm  float32, 1 element
-    coef   float32, 1 element (None if the call had no max_norm)
+    coef   float32, 1 element (None if the last call had no max_norm; what a
+           step prepared with this object then reads is 1, or 0 and NaN by the
+           formula where the norm is infinite or NaN)
 
     Calls that may run at the same time, replays of two captured graphs among
     them, need a GradNorm each."""
@@ -63,7 +68,8 @@ class GradNorm:
         """Issue a norm call whose outputs are this object's."""
         p = self._buf.data_ptr()
         clips = max_norm is not None
-        args += (float(max_norm) if clips else 0.0, p, p + 8, p + 12 if clips else None)
+        # the coefficient is always written: a prepared step may read it at any later issue
+        args += (float(max_norm) if clips else sys.float_info.max, p, p + 8, p + 12)
         _issue(name, self.device, stream, *args, *((p + 16,) if workspace else ()))
         self.has_coef = clips
         return self
