@@ -152,7 +152,8 @@ def fsdp_grad_norm_units(units, rank, fp32_reduce, max_norm=None, out=None, stre
     """Norm over rank `rank`'s shards of the averaged gradient of `units`, in the
     pass that reduces them.  A unit is a dict as fsdp_step_units has it:
     rank_grads, and master or shard_numel for the shard's size; with grad_shard
-    (the dtype of fsdp_reduce_scatter_local) the averaged shard is stored there.
+    (of that size, the dtype of fsdp_reduce_scatter_local) the averaged shard is
+    stored there.
     All units share world, rank and dtype.  Returns the GradNorm."""
     _max_norm(max_norm)
     if not units:
@@ -161,15 +162,13 @@ def fsdp_grad_norm_units(units, rank, fp32_reduce, max_norm=None, out=None, stre
     table = (N.NormUnit * len(units))()
     keep, tensors, gdt = [], [], None
     for k, u in enumerate(units):
-        shard = u.get("grad_shard")
-        if shard is not None:
-            S = shard.numel()
-        elif u.get("master") is not None:
-            S = u["master"].numel()
-        elif u.get("shard_numel") is not None:
-            S = int(u["shard_numel"])
-        else:
+        shard, master, given = u.get("grad_shard"), u.get("master"), u.get("shard_numel")
+        sizes = [t.numel() for t in (shard, master) if t is not None] + ([int(given)] if given is not None else [])
+        if not sizes:
             raise ValueError("units[%d] needs grad_shard, master or shard_numel" % k)
+        S = sizes[0]
+        if any(n != S for n in sizes):           # rank r's block of a gradient begins at r * S
+            raise ValueError("units[%d]: grad_shard, master and shard_numel give different sizes: %s" % (k, sizes))
         grads, w, g_dt = _grads(u["rank_grads"], S)
         if w != world:
             raise ValueError("units[%d] has %d ranks, units[0] %d" % (k, w, world))
