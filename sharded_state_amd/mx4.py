@@ -239,11 +239,15 @@ def _space(nbytes, device, stream):
 def fsdp_mx4_linear(x, w, out=None, stream=None):
     """y = x W^T for x [tokens, in] and W an Mx4 [out, in]: x is quantised along
     its features on the way (for a few tokens within the one launch).  y has x's
-    dtype unless `out` says otherwise."""
+    dtype unless `out` says otherwise, and no graph: where grad mode is on, an x
+    that requires grad is refused."""
     if not isinstance(w, Mx4):
         raise TypeError("w must be an Mx4")
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != w.cols:
         raise ValueError("x must be a matrix of %d columns" % w.cols)
+    if x.requires_grad and torch.is_grad_enabled():
+        raise ValueError("x requires grad, and y would carry none: call under torch.no_grad() or detach x, and take "
+                         "the gradients from fsdp_mx4_linear_grads")
     m, k, ldx = _matrix(x, "x")
     device = x.device
     out, ldo = _result(out, m, w.rows, x.dtype, device, stream)
