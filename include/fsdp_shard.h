@@ -431,6 +431,10 @@ FSDP_API int fsdp_step_units_clipped(const fsdp_unit* units, int32_t n_units, in
  * bytes, two to a byte, the first in the low nibble, codes 0 behind column C;
  * scales are R * nb bytes.  A flat shard is a matrix of one row.  Codes are
  * 16-byte aligned (FSDP_E_INVAL otherwise).
+ *
+ * No output (or workspace) may overlap another buffer of its call
+ * (FSDP_E_ALIAS).  Rows with gaps overlap where their elements do: column
+ * slices of one buffer, with one ld, may be x and out.
  * ------------------------------------------------------------------------ */
 #define FSDP_MX4_MAX_K (1 << 23)   /* longest summed axis of a product */
 

@@ -38,40 +38,71 @@ int check_sum(const char* fn, int64_t k) {
     return FSDP_OK;
 }
 
-// A matrix with strided rows, recorded as a range; `used`: it is read or written.
+// A buffer of a product: `rows` rows of `n` bytes, `pitch` bytes from one to the next.
+struct Span {
+    uintptr_t lo;
+    uint64_t n, pitch, rows;
+};
+Span span(const void* p, uint64_t bytes) { return Span{(uintptr_t)p, bytes, bytes, 1}; }
+
+bool meet(const Span& x, const Span& y) {
+    if (x.n == 0 || y.n == 0 || x.rows == 0 || y.rows == 0) return false;
+    if (x.lo >= y.lo + (y.rows - 1) * y.pitch + y.n || y.lo >= x.lo + (x.rows - 1) * x.pitch + x.n) return false;
+    const Span &a = x.rows > 1 ? x : y, &b = x.rows > 1 ? y : x;
+    if (a.rows == 1 || (b.rows > 1 && b.pitch != a.pitch)) return true;
+    // where b's rows begin within a's pitch: column slices of one buffer lie side by side there
+    const uint64_t d = b.lo >= a.lo ? (b.lo - a.lo) % a.pitch : (a.pitch - (a.lo - b.lo) % a.pitch) % a.pitch;
+    return d < a.n || d + b.n > a.pitch;
+}
+
+// No two outputs meet and no output meets an input.
+bool apart(const std::vector<Span>& outs, const std::vector<Span>& ins) {
+    for (size_t i = 0; i < outs.size(); ++i) {
+        for (size_t j = 0; j < i; ++j)
+            if (meet(outs[i], outs[j])) return false;
+        for (const Span& r : ins)
+            if (meet(outs[i], r)) return false;
+    }
+    return true;
+}
+
+// A matrix with strided rows, recorded as a span; `used`: it is read or written.
 struct Rows {
     int64_t ld = 0;
 };
 int check_rows(const char* fn, const char* name, const void* p, int dt, int64_t rows, int64_t cols, int64_t ld,
-               bool used, Rows& r, std::vector<Range>& ranges) {
+               bool used, Rows& r, std::vector<Span>& spans) {
     if (used && !p) return fail(FSDP_E_INVAL, "%s: %s is NULL", fn, name);
     if (rows > 1 && ld < cols) return fail(FSDP_E_INVAL, "%s: the rows of %s overlap", fn, name);
     if (rows > 1 && ld > kMaxElems / rows) return fail(FSDP_E_SIZE, "%s: %s is too large", fn, name);
     r.ld = rows > 1 ? ld : cols;
-    if (rows > 0 && cols > 0) ranges.push_back(range(p, (rows - 1) * r.ld + cols, dt_size(dt)));
+    const uint64_t es = dt_size(dt);
+    if (rows > 0 && cols > 0)
+        spans.push_back(Span{(uintptr_t)p, (uint64_t)cols * es, (uint64_t)r.ld * es, (uint64_t)rows});
     return FSDP_OK;
 }
 
-// A matrix in blocks, recorded as ranges.
+// A matrix in blocks, recorded as spans.
 int check_blocked(const char* fn, const char* name, const void* codes, const void* scales, int64_t rows, int64_t cols,
-                  std::vector<Range>& ranges) {
+                  std::vector<Span>& spans) {
     if (rows > 0 && cols > 0 && (!codes || !scales)) return fail(FSDP_E_INVAL, "%s: %s is NULL", fn, name);
     if (!aligned16(codes)) return fail(FSDP_E_INVAL, "%s: codes of %s must be 16-byte aligned", fn, name);
-    ranges.push_back(range(codes, rows * mx4_blocks(cols), 16));
-    ranges.push_back(range(scales, rows * mx4_blocks(cols), 1));
+    const uint64_t blocks = (uint64_t)rows * (uint64_t)mx4_blocks(cols);
+    spans.push_back(span(codes, blocks * 16));
+    spans.push_back(span(scales, blocks));
     return FSDP_OK;
 }
 
 // Bytes of a matrix in blocks in a workspace, codes then scales, so that the next one is aligned.
 int64_t blocked_bytes(int64_t rows, int64_t cols) { return (rows * mx4_blocks(cols) * 17 + 15) / 16 * 16; }
 
-int check_space(const char* fn, void* ws, int64_t have, int64_t need, std::vector<Range>& ranges) {
+int check_space(const char* fn, void* ws, int64_t have, int64_t need, std::vector<Span>& spans) {
     if (need == 0) return FSDP_OK;
     if (!ws) return fail(FSDP_E_INVAL, "%s: workspace is NULL", fn);
     if (!aligned16(ws)) return fail(FSDP_E_INVAL, "%s: workspace must be 16-byte aligned", fn);
     if (have < need)
         return fail(FSDP_E_SIZE, "%s: the workspace has %lld bytes, %lld are needed", fn, (long long)have, (long long)need);
-    ranges.push_back(range(ws, need, 1));
+    spans.push_back(span(ws, (uint64_t)need));
     return FSDP_OK;
 }
 
@@ -226,7 +257,7 @@ int fsdp_mx4_linear(const void* x, fsdp_dtype x_dt, int64_t m, int64_t k, int64_
         if (!rc) rc = check_sum(fn, k);
         if (rc) return rc;
         if (m == 0 || n == 0) return ok();
-        std::vector<Range> ins, outs;
+        std::vector<Span> ins, outs;
         Rows xr, yr;
         rc = check_rows(fn, "x", x, x_dt, m, k, ldx, k > 0, xr, ins);
         if (!rc) rc = check_rows(fn, "out", out, out_dt, m, n, ldo, true, yr, outs);
@@ -237,7 +268,7 @@ int fsdp_mx4_linear(const void* x, fsdp_dtype x_dt, int64_t m, int64_t k, int64_
             rc = check_space(fn, workspace, workspace_bytes, blocked_bytes(m, k), outs);
             if (rc) return rc;
         }
-        if (!disjoint(outs, ins)) return fail(FSDP_E_ALIAS, "%s: an output or the workspace overlaps another buffer", fn);
+        if (!apart(outs, ins)) return fail(FSDP_E_ALIAS, "%s: an output or the workspace overlaps another buffer", fn);
         const int64_t nb = mx4_blocks(k);
         (void)hipGetLastError();
         hipError_t e;
@@ -286,7 +317,7 @@ int fsdp_mx4_linear_grads(const void* dy, fsdp_dtype dy_dt, int64_t lddy, const 
         if (rc) return rc;
         const bool want_dx = dx && m > 0 && k > 0, want_dw = dw && n > 0 && k > 0;
         if (!want_dx && !want_dw) return ok();
-        std::vector<Range> ins, outs;
+        std::vector<Span> ins, outs;
         Rows dyr, xr, dxr, dwr;
         rc = check_rows(fn, "dy", dy, dy_dt, m, n, lddy, m > 0 && n > 0, dyr, ins);
         if (!rc && want_dw) rc = check_rows(fn, "x", x, x_dt, m, k, ldx, m > 0, xr, ins);
@@ -298,7 +329,7 @@ int fsdp_mx4_linear_grads(const void* dy, fsdp_dtype dy_dt, int64_t lddy, const 
                              (want_dx ? blocked_bytes(m, n) : 0) + (want_dw ? blocked_bytes(n, m) + blocked_bytes(k, m) : 0),
                              outs);
         if (rc) return rc;
-        if (!disjoint(outs, ins)) return fail(FSDP_E_ALIAS, "%s: an output or the workspace overlaps another buffer", fn);
+        if (!apart(outs, ins)) return fail(FSDP_E_ALIAS, "%s: an output or the workspace overlaps another buffer", fn);
         const int64_t nbn = mx4_blocks(n), nbm = mx4_blocks(m);
         uint8_t* at = (uint8_t*)workspace;
         uint8_t *q = nullptr, *sq = nullptr, *qt = nullptr, *st = nullptr, *xt = nullptr, *sx = nullptr;
@@ -345,13 +376,13 @@ int fsdp_mx4_matmul(const void* a_codes, const void* a_scales, const void* b_cod
         rc = check_sum(fn, k);
         if (rc) return rc;
         if (m == 0 || n == 0) return ok();
-        std::vector<Range> ins, outs;
+        std::vector<Span> ins, outs;
         Rows r;
         rc = check_rows(fn, "out", out, out_dt, m, n, ldo, true, r, outs);
         if (!rc) rc = check_blocked(fn, "a", a_codes, a_scales, m, k, ins);
         if (!rc) rc = check_blocked(fn, "b", b_codes, b_scales, n, k, ins);
         if (rc) return rc;
-        if (!disjoint(outs, ins)) return fail(FSDP_E_ALIAS, "%s: out overlaps an operand", fn);
+        if (!apart(outs, ins)) return fail(FSDP_E_ALIAS, "%s: out overlaps an operand", fn);
         const Mx4Product p{(const uint8_t*)a_codes, (const uint8_t*)a_scales, (const uint8_t*)b_codes,
                            (const uint8_t*)b_scales, m, n, mx4_blocks(k), (int)out_dt, out, r.ld, cu_count(), stream};
         (void)hipGetLastError();
