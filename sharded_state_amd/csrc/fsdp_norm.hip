@@ -123,20 +123,6 @@ __global__ __launch_bounds__(kFinishThreads) void k_norm_finish(const double* __
     if (threadIdx.x == 0) write_norm(s, o);
 }
 
-// The average as finish() defines it.  For a 16-bit fp16 average the product is
-// kept apart from the rounding: fused into one mixed-precision fma the compiler
-// adds +0 to it, and an average of -0 loses its sign.
-template <int NW, int GF, bool FP32R>
-__device__ __forceinline__ float average(float acc, const ReduceScalars& rs) {
-    if constexpr (NW > 0 && GF == FSDP_F16 && !FP32R) {
-        float y = acc * rs.inv_n;
-        asm("" : "+v"(y));
-        return round_to<GF>(y);
-    } else {
-        return finish<NW, GF, FP32R>(acc, rs);
-    }
-}
-
 // The sum over the averaged gradient of a table of units: the reduce-scatter's
 // fold (fsdp_device.h) with the squares added as its epilogue, and the shard
 // stored where the caller wants it.  Vectors in the group layout for an fp32
@@ -171,7 +157,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_units(NormUnits<NW> B, Reduce
                 if (B.wide[u]) reduce8<NW, GF, FP32R, true, kGroup>(gp, world, vi, x);
                 else reduce8_any<NW, GF, FP32R>(gp, world, vi, x);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) x[k] = average<NW, GF, FP32R>(x[k], rs);
+                for (int k = 0; k < 8; ++k) x[k] = finish<NW, GF, FP32R>(x[k], rs);
                 if (out && B.wide[u]) store8x<OF, kGroup>(out, vi, x);
                 else if (out) store8_any<OF>((char*)out + vi * (OF == FSDP_F32 ? 32 : 16), x);
 #pragma unroll
@@ -183,7 +169,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_units(NormUnits<NW> B, Reduce
         } else {
             const int64_t i = nvec * 8 + (j - tv) * kThreads + threadIdx.x;
             if (i < B.S[u]) {
-                const float x = average<NW, GF, FP32R>(reduce1<NW, GF, FP32R>(gp, world, i), rs);
+                const float x = finish<NW, GF, FP32R>(reduce1<NW, GF, FP32R>(gp, world, i), rs);
                 if (out) store1<OF>(out, i, x);
                 a = sq(x, a);
             }
