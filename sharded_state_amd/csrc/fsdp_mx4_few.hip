@@ -211,11 +211,22 @@ __global__ __launch_bounds__(64 * NW) void k_mx4_few(Mx4Few p) {
     mx4_few<XF, NW>(p);
 }
 
+// More rows of W than a launch's work items allow go in launches of kFewRows.
+constexpr int64_t kFewRows = 1 << 26;
 template <int XF, int NW>
 static hipError_t few(const Mx4Few& p) {
     const unsigned lds = (unsigned)few_lds<XF, NW>((int)p.nb, (int)p.m).bytes;
-    launch_lds(k_mx4_few<XF, NW>, dim3((unsigned)((p.n + 15) / 16)), dim3(64 * NW), lds, (hipStream_t)p.stream, p);
-    return hipGetLastError();
+    for (int64_t n0 = 0; n0 < p.n; n0 += kFewRows) {
+        Mx4Few c = p;
+        c.n = p.n - n0 < kFewRows ? p.n - n0 : kFewRows;
+        c.w = p.w + n0 * p.nb * 16;
+        c.sw = p.sw + n0 * p.nb;
+        c.out = (char*)p.out + n0 * dt_bytes(p.dt);
+        launch_lds(k_mx4_few<XF, NW>, dim3((unsigned)((c.n + 15) / 16)), dim3(64 * NW), lds, (hipStream_t)p.stream, c);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 // Waves.  x quantised on the way: 8, or 4 where no wave would have a run of its own
@@ -230,7 +241,6 @@ static hipError_t few_of(const Mx4Few& p) {
 }
 
 hipError_t launch_mx4_few(const Mx4Few& p) {
-    if (p.n / 16 >= (int64_t(1) << 32) / 512 - 1) return hipErrorInvalidValue;   // work items of a launch
     if (p.sx) return few_of<kBlocked>(p);
     if (p.xdt == FSDP_F32) return few_of<FSDP_F32>(p);
     if (p.xdt == FSDP_F16) return few_of<FSDP_F16>(p);

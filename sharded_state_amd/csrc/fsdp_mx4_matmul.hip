@@ -77,12 +77,13 @@ hipError_t launch_mx4_matmul(const Mx4Product& p) {
 //   4096 x 4096 x 4096  83.7  64: 152.7  128: 106.1  256: 78.8 (256 + 256)
 //   128 x 8192 x 8192   80.9  64: 101.3  128: 82.9   256: 102.9 (32 + 1024)
 hipError_t launch_mx4_two(const Mx4Product& a, const Mx4Product& b) {
-    if (side(a) == 16 || side(b) == 16) {
+    const int64_t enough = a.cus * 5 / 8, ta = tiles(a, 256), tb = tiles(b, 256);
+    // apart too where the tiles (four times as many of 128) might pass a launch's work items
+    if (side(a) == 16 || side(b) == 16 || ta + tb > (1 << 20)) {
         hipError_t e = launch_mx4_matmul(a);
         return e == hipSuccess ? launch_mx4_matmul(b) : e;
     }
     const Mx4Product &x = a.nb >= b.nb ? a : b, &y = a.nb >= b.nb ? b : a;
-    const int64_t enough = a.cus * 5 / 8, ta = tiles(a, 256), tb = tiles(b, 256);
     if (ta + tb >= enough && ta >= enough / 2 && tb >= enough / 2) return launch_two<256, 256, 2, 4, 2>(x, y);
     if (tiles(a, 128) + tiles(b, 128) >= enough) return launch_two<128, 128, 2, 2, 4>(x, y);
     return launch_two<64, 64, 2, 2, 4>(x, y);

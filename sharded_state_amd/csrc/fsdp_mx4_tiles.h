@@ -308,19 +308,34 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx4_two(Mx4Product a, Mx4Produ
 
 template <int F, int BM, int BN, int WM, int WN, int NS>
 static hipError_t launch_tiles(const Mx4Product& p) {
+    // a launch holds fewer than 2^32 work items; more tiles go in parts of the result
+    constexpr int64_t kMost = (int64_t(1) << 32) / (64 * WM * WN) - 1;
     const int64_t tm = (p.m + BM - 1) / BM, tn = (p.n + BN - 1) / BN;
-    // a launch holds fewer than 2^32 work items
-    if (tm * tn >= (int64_t(1) << 32) / (64 * WM * WN)) return hipErrorInvalidValue;
-    launch(k_mx4_tiles<F, BM, BN, WM, WN, NS>, dim3((unsigned)(tm * tn)), dim3(64 * WM * WN), (hipStream_t)p.stream,
-           p, (uint32_t)tm, (uint32_t)tn);
-    return hipGetLastError();
+    const int64_t pn = tn < kMost ? tn : kMost, pm = kMost / pn < tm ? kMost / pn : tm;
+    for (int64_t i = 0; i < tm; i += pm)
+        for (int64_t j = 0; j < tn; j += pn) {
+            const int64_t m0 = i * BM, n0 = j * BN, cm = tm - i < pm ? tm - i : pm, cn = tn - j < pn ? tn - j : pn;
+            Mx4Product c = p;
+            c.a = p.a + m0 * p.nb * 16;
+            c.sa = p.sa + m0 * p.nb;
+            c.b = p.b + n0 * p.nb * 16;
+            c.sb = p.sb + n0 * p.nb;
+            c.m = p.m - m0 < cm * BM ? p.m - m0 : cm * BM;
+            c.n = p.n - n0 < cn * BN ? p.n - n0 : cn * BN;
+            c.out = (char*)p.out + (m0 * p.ldo + n0) * dt_bytes(p.dt);
+            launch(k_mx4_tiles<F, BM, BN, WM, WN, NS>, dim3((unsigned)(cm * cn)), dim3(64 * WM * WN),
+                   (hipStream_t)p.stream, c, (uint32_t)cm, (uint32_t)cn);
+            hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+    return hipSuccess;
 }
 
+// Of few enough tiles for one launch (launch_mx4_two).
 template <int BM, int BN, int WM, int WN, int NS>
 static hipError_t launch_two(const Mx4Product& a, const Mx4Product& b) {
     const int64_t am = (a.m + BM - 1) / BM, an = (a.n + BN - 1) / BN, bm = (b.m + BM - 1) / BM, bn = (b.n + BN - 1) / BN;
     const int64_t first = (am * an + 7) / 8 * 8;
-    if (first + bm * bn >= (int64_t(1) << 32) / (64 * WM * WN)) return hipErrorInvalidValue;
     launch(k_mx4_two<BM, BN, WM, WN, NS>, dim3((unsigned)(first + bm * bn)), dim3(64 * WM * WN), (hipStream_t)a.stream,
            a, b, (uint32_t)first, (uint32_t)am, (uint32_t)an, (uint32_t)bm, (uint32_t)bn);
     return hipGetLastError();
