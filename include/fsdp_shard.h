@@ -442,7 +442,8 @@ FSDP_API int fsdp_step_units_clipped(const fsdp_unit* units, int32_t n_units, in
  * with codes and scales not NULL in blocks along its rows, with codes_t and
  * scales_t not NULL in blocks along its columns, as the matrix of cols rows and
  * `rows` columns that is its transpose (what the gradients of a product sum
- * over); both at once read src once where they can. */
+ * over); both at once read src once where they can.  FSDP_E_SIZE for more than
+ * 2^31 tiles of 128 x 128 elements along the columns. */
 FSDP_API int fsdp_mx4_quantize(const void* src, fsdp_dtype dt, int64_t rows, int64_t cols, int64_t ld,
                                void* codes, void* scales, void* codes_t, void* scales_t, void* stream);
 

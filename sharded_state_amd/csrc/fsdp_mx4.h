@@ -13,6 +13,13 @@ namespace fsdp {
 constexpr int kMx4Block = 32;                            // elements that share a scale
 inline int64_t mx4_blocks(int64_t cols) { return (cols + kMx4Block - 1) / kMx4Block; }
 
+// Tiles that blocks along the columns are made in; their number is held in 32 bits.
+constexpr int kMx4Tile = 128;
+constexpr int64_t kMx4MaxColTiles = int64_t(1) << 31;
+inline int64_t mx4_col_tiles(int64_t rows, int64_t cols) {
+    return ((rows + kMx4Tile - 1) / kMx4Tile) * ((cols + kMx4Tile - 1) / kMx4Tile);
+}
+
 struct Mx4Quant {
     const void* src;               // rows x cols, ld elements from row to row
     int dt;

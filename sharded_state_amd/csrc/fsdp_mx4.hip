@@ -65,10 +65,11 @@ __global__ __launch_bounds__(kThreads) void k_mx4_rows(const char* __restrict__ 
 // turn; XCD x takes one run of tiles down the columns, so what neighbouring
 // tiles write to a line of the transpose (64 bytes of codes, 4 of scales each)
 // meets in one L2.
-constexpr int kTile = 128;
+constexpr int kTile = kMx4Tile;
 struct Mx4Cols {
     Mx4Quant q;
     uint32_t tiles_r, tiles;       // tiles down the rows, and in all
+    uint32_t from;                 // the launch's first tile
 };
 // Tile number `b` of job `j`, in the order of the launch.
 template <int F, bool ROWS>
@@ -172,8 +173,10 @@ __global__ __launch_bounds__(kThreads) void k_mx4_cols(Mx4Cols a, Mx4Cols also) 
     // the tile as it is, later its codes (8.8 KB)
     __shared__ __attribute__((aligned(16))) uint8_t lds[kTile * kTile * (F == FSDP_F32 ? 4 : 2)];
     const uint32_t first = (a.tiles + 7) & ~7u;
-    if (!PAIR || blockIdx.x < first) {
-        if (!PAIR || blockIdx.x < a.tiles) cols_tile<F, ROWS>(a, blockIdx.x, lds);
+    if constexpr (!PAIR) {
+        cols_tile<F, ROWS>(a, a.from + blockIdx.x, lds);
+    } else if (blockIdx.x < first) {
+        if (blockIdx.x < a.tiles) cols_tile<F, ROWS>(a, blockIdx.x, lds);
     } else {
         cols_tile<F, false>(also, blockIdx.x - first, lds);
     }
@@ -256,27 +259,35 @@ static unsigned capped(int64_t want) {
     return (unsigned)(want < 1 ? 1 : (want < cap ? want : cap));
 }
 
-constexpr int64_t kMaxTiles = (1 << 23) - 8;      // two jobs of a launch hold fewer than 2^32 work items
+// Workgroups of a column launch, a multiple of 8: fewer than 2^32 work items.
+constexpr int64_t kMaxTiles = (1 << 23) - 8;
 
-static bool cols_job(const Mx4Quant& q, Mx4Cols& j) {
-    const int64_t tr = (q.rows + kTile - 1) / kTile, tc = (q.cols + kTile - 1) / kTile;
-    if (tr > kMaxTiles / tc) return false;
-    j = Mx4Cols{q, (uint32_t)tr, (uint32_t)(tr * tc)};
-    return true;
+static Mx4Cols cols_job(const Mx4Quant& q) {
+    return Mx4Cols{q, (uint32_t)((q.rows + kTile - 1) / kTile), (uint32_t)mx4_col_tiles(q.rows, q.cols), 0};
 }
 
 template <int F>
 static hipError_t quantize(const Mx4Quant& q, const Mx4Quant* also, hipStream_t st) {
     const char* src = (const char*)q.src;
+    const dim3 th(kThreads);
     if (q.codes_t) {
-        Mx4Cols a, b{};
-        if (!cols_job(q, a) || (also && !cols_job(*also, b))) return hipErrorInvalidValue;
-        const dim3 g(also ? ((a.tiles + 7) & ~7u) + b.tiles : a.tiles), th(kThreads);
-        if (q.codes && also) launch(k_mx4_cols<F, true, true>, g, th, st, a, b);
-        else if (q.codes) launch(k_mx4_cols<F, true, false>, g, th, st, a, b);
-        else if (also) launch(k_mx4_cols<F, false, true>, g, th, st, a, b);
-        else launch(k_mx4_cols<F, false, false>, g, th, st, a, b);
-        return hipGetLastError();
+        Mx4Cols a = cols_job(q), b{};
+        if (also) b = cols_job(*also);
+        const int64_t both = ((int64_t)a.tiles + 7) / 8 * 8 + b.tiles;
+        if (also && both <= kMaxTiles) {
+            if (q.codes) launch(k_mx4_cols<F, true, true>, dim3((unsigned)both), th, st, a, b);
+            else launch(k_mx4_cols<F, false, true>, dim3((unsigned)both), th, st, a, b);
+            return hipGetLastError();
+        }
+        for (int64_t t = 0; t < a.tiles; t += kMaxTiles) {
+            const dim3 g((unsigned)(a.tiles - t < kMaxTiles ? a.tiles - t : kMaxTiles));
+            a.from = (uint32_t)t;
+            if (q.codes) launch(k_mx4_cols<F, true, false>, g, th, st, a, b);
+            else launch(k_mx4_cols<F, false, false>, g, th, st, a, b);
+            hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        return also ? quantize<F>(*also, nullptr, st) : hipSuccess;
     }
     int64_t rows = q.rows, cols = q.cols;
     if (q.ld == cols && cols % kMx4Block == 0) {      // whole blocks row after row: one long row
@@ -284,8 +295,8 @@ static hipError_t quantize(const Mx4Quant& q, const Mx4Quant* also, hipStream_t 
         rows = 1;
     }
     const int64_t nb = mx4_blocks(cols);
-    launch(k_mx4_rows<F>, dim3(capped((rows * nb * 4 + kThreads * kRowsU<F> - 1) / (kThreads * kRowsU<F>))), dim3(kThreads), st, src, rows,
-           cols, q.ld, nb, q.codes, q.scales);
+    launch(k_mx4_rows<F>, dim3(capped((rows * nb * 4 + kThreads * kRowsU<F> - 1) / (kThreads * kRowsU<F>))), th, st,
+           src, rows, cols, q.ld, nb, q.codes, q.scales);
     return hipGetLastError();
 }
 

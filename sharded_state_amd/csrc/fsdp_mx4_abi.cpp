@@ -32,6 +32,14 @@ int check_matrix(const char* fn, int64_t rows, int64_t cols) {
     return FSDP_OK;
 }
 
+// A matrix to be quantised along its columns.
+int check_columns(const char* fn, int64_t rows, int64_t cols) {
+    if (rows > 0 && cols > 0 && mx4_col_tiles(rows, cols) > kMx4MaxColTiles)
+        return fail(FSDP_E_SIZE, "%s: blocks along the columns of %lld x %lld: too many tiles", fn, (long long)rows,
+                    (long long)cols);
+    return FSDP_OK;
+}
+
 // Longest summed axis of a product.
 int check_sum(const char* fn, int64_t k) {
     if (k > FSDP_MX4_MAX_K) return fail(FSDP_E_SIZE, "%s: a sum of %lld > %d terms", fn, (long long)k, FSDP_MX4_MAX_K);
@@ -139,6 +147,8 @@ int fsdp_mx4_quantize(const void* src, fsdp_dtype dt, int64_t rows, int64_t cols
         if (!aligned16(codes) || !aligned16(codes_t))
             return fail(FSDP_E_INVAL, "%s: codes must be 16-byte aligned", fn);
         if (!src) return fail(FSDP_E_INVAL, "%s: src is NULL", fn);
+        if (codes_t) rc = check_columns(fn, rows, cols);
+        if (rc) return rc;
         const int64_t nb = mx4_blocks(cols), nbr = mx4_blocks(rows);
         std::vector<Range> outs;
         if (codes) {
@@ -314,6 +324,8 @@ int fsdp_mx4_linear_grads(const void* dy, fsdp_dtype dy_dt, int64_t lddy, const 
         if (!rc) rc = check_matrix(fn, n, k);
         if (!rc && dx) rc = check_sum(fn, n);
         if (!rc && dw) rc = check_sum(fn, m);
+        if (!rc && dw) rc = check_columns(fn, m, n);
+        if (!rc && dw) rc = check_columns(fn, m, k);
         if (rc) return rc;
         const bool want_dx = dx && m > 0 && k > 0, want_dw = dw && n > 0 && k > 0;
         if (!want_dx && !want_dw) return ok();
