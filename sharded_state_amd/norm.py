@@ -162,13 +162,19 @@ def fsdp_grad_norm_units(units, rank, fp32_reduce, max_norm=None, out=None, stre
     table = (N.NormUnit * len(units))()
     keep, tensors, gdt = [], [], None
     for k, u in enumerate(units):
-        shard, master, given = u.get("grad_shard"), u.get("master"), u.get("shard_numel")
-        sizes = [t.numel() for t in (shard, master) if t is not None] + ([int(given)] if given is not None else [])
-        if not sizes:
+        shard, S = u.get("grad_shard"), u.get("shard_numel")
+        if S is not None:
+            S = int(S)
+        for t in (shard, u.get("master")):
+            if t is None:
+                continue
+            if S is None:
+                S = t.numel()
+            elif t.numel() != S:                 # rank r's block of a gradient begins at r * S
+                raise ValueError("units[%d]: grad_shard, master and shard_numel give the sizes %d and %d"
+                                 % (k, S, t.numel()))
+        if S is None:
             raise ValueError("units[%d] needs grad_shard, master or shard_numel" % k)
-        S = sizes[0]
-        if any(n != S for n in sizes):           # rank r's block of a gradient begins at r * S
-            raise ValueError("units[%d]: grad_shard, master and shard_numel give different sizes: %s" % (k, sizes))
         grads, w, g_dt = _grads(u["rank_grads"], S)
         if w != world:
             raise ValueError("units[%d] has %d ranks, units[0] %d" % (k, w, world))
