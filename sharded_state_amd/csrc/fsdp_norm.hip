@@ -112,7 +112,7 @@ constexpr int kFinishThreads = 1024;
 constexpr int kFinishU = kNormSlots / kFinishThreads;
 __global__ __launch_bounds__(kFinishThreads) void k_norm_finish(const double* __restrict__ partial, int n, NormOut o) {
     double s = 0.0;
-    for (int i0 = threadIdx.x; i0 < n; i0 += kFinishThreads * kFinishU) {
+    for (int64_t i0 = threadIdx.x; i0 < n; i0 += kFinishThreads * kFinishU) {
         double v[kFinishU];
 #pragma unroll
         for (int u = 0; u < kFinishU; ++u) v[u] = i0 + u * kFinishThreads < n ? partial[i0 + u * kFinishThreads] : 0.0;
