@@ -10,7 +10,7 @@ the calls a user makes of ``sharded_state_amd``; ``own`` says which of the two
               into the full buffer
   linear      y = x W^T with W in 8-bit blocks and x quantised on the way
   layer       the norm and the product that reads it
-  grads       the gradients of that product: dx and dw
+  grads       the gradients of that product: dx and dw, in the type of x as the reduce-scatter takes them
 
 8-bit blocks: 128 elements of a row (of a 128 x 128 tile with ``tile``) share a power of two 2^e, e the
 smallest whole number from -126 on with max|x| <= 448 * 2^e, and each is the e4m3 number nearest to
@@ -213,7 +213,7 @@ def _plain(s):
         h, r, y = _norm(s)
         return dict(h=h, y=(_q32(y) @ _values(*_given(s["w"]), s["k"]).t()).to(s["x"].dtype))
     dx = (_q32(s["dy"]) @ _values(*_given(s["w"]), s["n"]).t()).to(s["x"].dtype)
-    return dict(dx=dx, dw=_q32(s["dy"].t()) @ _q32(s["x"].t()).t())
+    return dict(dx=dx, dw=(_q32(s["dy"].t()) @ _q32(s["x"].t()).t()).to(s["x"].dtype))
 
 
 # ------------------------------------------------------------------ the framework's calls
@@ -236,8 +236,7 @@ def _mine(s):
     if kind == "layer":
         o = ss.fsdp_rms_norm_fp8(s["x"], s["weight"], s["residual"], eps=EPS)
         return dict(h=o.h, y=ss.fsdp_fp8_linear(o.q, ss.Fp8(*s["w"], s["k"], tile=s["tile"]), dtype=s["x"].dtype))
-    dx, dw = ss.fsdp_fp8_linear_grads(s["dy"], s["x"], ss.Fp8(*s["w"], s["n"], tile=s["tile"]),
-                                      dw_dtype=torch.float32)
+    dx, dw = ss.fsdp_fp8_linear_grads(s["dy"], s["x"], ss.Fp8(*s["w"], s["n"], tile=s["tile"]))
     return dict(dx=dx, dw=dw)
 
 
@@ -262,7 +261,7 @@ def work(case):
         return dict(bytes=m * k * b + w + m * n * b, flops=2 * m * n * k)
     if kind == "layer":
         return dict(bytes=3 * m * k * b + k * b + w + m * n * b, flops=2 * m * n * k + 8 * m * k)
-    return dict(bytes=m * n * b + 2 * m * k * b + w + 4 * n * k, flops=4 * m * n * k)
+    return dict(bytes=m * n * b + 2 * m * k * b + w + n * k * b, flops=4 * m * n * k)
 
 
 # ------------------------------------------------------------------ 64 bits, from the definitions
