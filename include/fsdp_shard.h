@@ -52,7 +52,7 @@ extern "C" {
 
 #define FSDP_API __attribute__((visibility("default")))
 
-#define FSDP_ABI_VERSION 10
+#define FSDP_ABI_VERSION 11
 #define FSDP_MAX_WORLD 128
 /* Bytes of the device scratch of fsdp_offload_step_units_noalloc (per device). */
 #define FSDP_OFFLOAD_SCRATCH_BYTES (32 << 20)
@@ -495,6 +495,125 @@ FSDP_API int fsdp_mx4_linear_grads(const void* dy, fsdp_dtype dy_dt, int64_t ldd
                                    const void* wt_codes, const void* wt_scales, fsdp_dtype dx_dt, void* dx,
                                    int64_t lddx, fsdp_dtype dw_dt, void* dw, int64_t lddw, void* workspace,
                                    int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit blocks: the compute copy in 129/128 byte an element, its all-gather,
+ * the product of matrices kept that way, and the norm in front of one.
+ *
+ * A block is 128 consecutive elements that share a power of two 2^e, with e the
+ * smallest whole number from -126 on such that max|x| <= 448 * 2^e; an element
+ * is the e4m3 number (sign, 4 bits of exponent with bias 7, 3 of significand,
+ * subnormals, no infinities, largest 448) nearest to x / 2^e, ties to the even
+ * one.  Nothing saturates.  Scale byte: e + 127.  A block that holds an infinity
+ * or a NaN has the scale byte 255 and codes 0, and stands for NaN.  With `tile`
+ * the 128 x 128 elements from a multiple of 128 rows and columns on share one
+ * scale in the same way.
+ *
+ * A matrix of R rows and C columns, nb = ceil(C / 128): codes are R * nb * 128
+ * bytes, codes 0 behind column C; scales are R * nb bytes, or ceil(R / 128) * nb
+ * with `tile`.  A flat shard is a matrix of one row.  Codes are 16-byte aligned
+ * (FSDP_E_INVAL otherwise).
+ *
+ * No output (or workspace) may overlap another buffer of its call
+ * (FSDP_E_ALIAS) but where a call says so.  Rows with gaps overlap where their
+ * elements do: column slices of one buffer, with one ld, may be x and out.
+ * Workspaces are device memory, 16-byte aligned, of at least the bytes that the
+ * call's ..._workspace function gives for its sizes (0: it may be NULL; -1 for
+ * sizes that the call refuses).  Calls that may run at the same time, replays of
+ * two captured graphs among them, need a workspace each.
+ * ------------------------------------------------------------------------ */
+#define FSDP_FP8_MAX_K (1 << 22)   /* longest summed axis of a product */
+#define FSDP_RMS_MAX_D (1 << 15)   /* most features of a norm */
+
+/* Quantise src (rows x cols of dt, ld elements from row to row, any alignment):
+ * with codes and scales not NULL in blocks along its rows, with codes_t and
+ * scales_t not NULL in blocks along its columns, as the matrix of cols rows and
+ * `rows` columns that is its transpose.  With `tile` (not 0) both hold the same
+ * values.  FSDP_E_SIZE for more than 2^31 tiles where it works in tiles. */
+FSDP_API int fsdp_fp8_quantize(const void* src, fsdp_dtype dt, int64_t rows, int64_t cols, int64_t ld,
+                               int32_t tile, void* codes, void* scales, void* codes_t, void* scales_t,
+                               void* stream);
+
+/* All-gather of quantised shards, each a matrix of one row, into the full
+ * buffer of dt: full_out[q * S + i] = element i of shard q, rounded to dt. */
+FSDP_API int fsdp_fp8_gather(const void* const* codes, const void* const* scales, int32_t world,
+                             int64_t shard_numel, fsdp_dtype dt, void* full_out, void* stream);
+
+/* All-gather of quantised shards as they are, into one matrix of one row and
+ * world * shard_numel columns.  shard_numel must be a multiple of 128
+ * (FSDP_E_SIZE), so that the shards' blocks join.  A shard that sits in its
+ * slot is not copied.  A tensor [n][k] of the unit with k and its offset
+ * multiples of 128 is then the matrix at codes + offset and
+ * scales + offset / 128. */
+FSDP_API int fsdp_fp8_gather_packed(const void* const* codes, const void* const* scales, int32_t world,
+                                    int64_t shard_numel, void* full_codes, void* full_scales, void* stream);
+
+/* out[i][j] = sum over k of A[i][k] * B[j][k] for A of m rows and B of n rows,
+ * k columns each, in tiles or not; fp32 sums, rounded once to out_dt; ldo
+ * elements from row to row of out (any alignment).  The matrix instruction adds
+ * eight consecutive products to a sum at a time, and of those eight it cuts off
+ * what lies under 2^-13 of the largest one's power of two (that of its factors'
+ * exponents): a result is off by less than 7 * 2^-13 of the sum of the eights'
+ * largest magnitudes, in practice 1.5e-5 of the result's norm with normally
+ * distributed operands.  A block that stands for NaN makes the row's (or
+ * column's) results NaN.  k = 0: zeros. */
+FSDP_API int64_t fsdp_fp8_matmul_workspace(int64_t m, int64_t n, int64_t k);
+FSDP_API int fsdp_fp8_matmul(const void* a_codes, const void* a_scales, int32_t a_tile, const void* b_codes,
+                             const void* b_scales, int32_t b_tile, int64_t m, int64_t n, int64_t k,
+                             fsdp_dtype out_dt, void* out, int64_t ldo, void* workspace,
+                             int64_t workspace_bytes, void* stream);
+
+/* y = x W^T: x [m][k] of x_dt (ldx elements from row to row, any alignment) is
+ * quantised along k as fsdp_fp8_quantize does it, and multiplied by W of n rows
+ * and k columns into out [m][n]. */
+FSDP_API int64_t fsdp_fp8_linear_workspace(int64_t m, int64_t n, int64_t k);
+FSDP_API int fsdp_fp8_linear(const void* x, fsdp_dtype x_dt, int64_t m, int64_t k, int64_t ldx,
+                             const void* w_codes, const void* w_scales, int32_t w_tile, int64_t n,
+                             fsdp_dtype out_dt, void* out, int64_t ldo, void* workspace,
+                             int64_t workspace_bytes, void* stream);
+
+/* Gradients of y = x W^T from dy [m][n] and x [m][k]: dx [m][k] = dy W and
+ * dw [n][k] = dy^T x, each the product of its operands quantised along the axis
+ * that it sums over (W, as wt, along its columns: a matrix of k rows and n
+ * columns; in tiles it is the forward's W, transposed).  dx or dw may be NULL:
+ * not wanted (then wt, or x, may be NULL).  m = 0 gives dw zeros. */
+FSDP_API int64_t fsdp_fp8_linear_grads_workspace(int64_t m, int64_t n, int64_t k, int32_t want_dx,
+                                                 int32_t want_dw);
+FSDP_API int fsdp_fp8_linear_grads(const void* dy, fsdp_dtype dy_dt, int64_t lddy, const void* x,
+                                   fsdp_dtype x_dt, int64_t ldx, int64_t m, int64_t n, int64_t k,
+                                   const void* wt_codes, const void* wt_scales, int32_t wt_tile,
+                                   fsdp_dtype dx_dt, void* dx, int64_t lddx, fsdp_dtype dw_dt, void* dw,
+                                   int64_t lddw, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Root-mean-square norm of m rows of d features, the residual's addition before
+ * it and 8-bit blocks behind it:
+ *   h    = x + residual, an fp32 sum rounded to h_dt; x as it is without a residual
+ *   rstd = 1 / sqrt(sum of h^2 / d + eps), sums in 64 bits
+ *   y    = (h * rstd) * weight in fp32, quantised along d as fsdp_fp8_quantize
+ *          does it, and where y is not NULL stored, rounded to y_dt
+ * x [m][d] of x_dt, residual and h [m][d] of h_dt (h is NULL exactly where
+ * residual is; h may be the residual itself, or x where their types are one),
+ * weight [d] of w_dt, rstd [m] or NULL; ld elements from row to row, any
+ * alignment.  eps is finite and not negative.  d is at most FSDP_RMS_MAX_D. */
+FSDP_API int fsdp_rms_norm_fp8(const void* x, fsdp_dtype x_dt, int64_t ldx, const void* residual,
+                               fsdp_dtype h_dt, int64_t ldr, int64_t m, int64_t d, const void* weight,
+                               fsdp_dtype w_dt, double eps, void* h, int64_t ldh, fsdp_dtype y_dt, void* y,
+                               int64_t ldy, void* codes, void* scales, float* rstd, void* stream);
+
+/* Its gradients from dy [m][d], h [m][d] and rstd [m]; the quantisation is passed
+ * through unchanged.  With g = dy * weight:
+ *   dx = rstd * (g - h * (rstd^2 * sum of g * h / d)) + dh   [m][d] of h_dt
+ *   dw = sum over the rows of dy * (h * rstd)                [d] of dw_dt
+ * dx is the gradient of x and of the residual alike.  dh [m][d] of h_dt, the
+ * gradient that h has from elsewhere, may be NULL.  dx or dw may be NULL: not
+ * wanted; dx may be dh itself, or dy where their types are one.  m = 0 gives dw
+ * zeros. */
+FSDP_API int64_t fsdp_rms_norm_grads_workspace(int64_t m, int64_t d, int32_t want_dw);
+FSDP_API int fsdp_rms_norm_grads(const void* dy, fsdp_dtype dy_dt, int64_t lddy, const void* h,
+                                 fsdp_dtype h_dt, int64_t ldh, int64_t m, int64_t d, const void* weight,
+                                 fsdp_dtype w_dt, const float* rstd, const void* dh, int64_t lddh, void* dx,
+                                 int64_t lddx, fsdp_dtype dw_dt, void* dw, void* workspace,
+                                 int64_t workspace_bytes, void* stream);
 
 /* Per-tensor views of the full buffer.  [P3] "The FSDP Unit" (use_orig_params):
  * tensor k is full[off_k : off_k + numel_k]; the padding belongs to no view.

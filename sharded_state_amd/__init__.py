@@ -34,6 +34,17 @@ from .mx4 import (  # noqa: F401
     fsdp_mx4_quantize,
     fsdp_mx4_views,
 )
+from .fp8 import (  # noqa: F401
+    Fp8,
+    fsdp_fp8_gather,
+    fsdp_fp8_gather_packed,
+    fsdp_fp8_linear,
+    fsdp_fp8_linear_grads,
+    fsdp_fp8_matmul,
+    fsdp_fp8_quantize,
+    fsdp_fp8_views,
+)
+from .rms import RmsNorm, fsdp_rms_norm_fp8, fsdp_rms_norm_grads  # noqa: F401
 from .norm import (  # noqa: F401
     GradNorm,
     fsdp_clip_grads,
@@ -62,5 +73,7 @@ __all__ = [
     "GradNorm", "fsdp_grad_norm", "fsdp_grad_norm_units", "fsdp_grad_norm_combine", "fsdp_clip_grads",
     "Mx4", "fsdp_mx4_quantize", "fsdp_mx4_gather", "fsdp_mx4_gather_packed", "fsdp_mx4_views", "fsdp_mx4_matmul",
     "fsdp_mx4_linear", "fsdp_mx4_linear_grads",
+    "Fp8", "fsdp_fp8_quantize", "fsdp_fp8_gather", "fsdp_fp8_gather_packed", "fsdp_fp8_views", "fsdp_fp8_matmul",
+    "fsdp_fp8_linear", "fsdp_fp8_linear_grads", "RmsNorm", "fsdp_rms_norm_fp8", "fsdp_rms_norm_grads",
     "UnitConfig", "from_fairseq", "from_bf16_mixed_precision",
 ]

@@ -13,7 +13,8 @@ LIB_PATH = os.path.join(_HERE, "libfsdp_shard.so")
 F32, F16, BF16 = 0, 1, 2
 OK, E_INVAL, E_DTYPE, E_SIZE, E_ALIAS, E_HIP, E_IO, E_FORMAT = 0, -1, -2, -3, -4, -5, -6, -7
 MAX_WORLD = 128
-ABI_VERSION = 10
+ABI_VERSION = 11
+RMS_MAX_D = 1 << 15
 NORM_WORKSPACE_BYTES = 32 << 10
 OFFLOAD_SCRATCH_BYTES = 32 << 20
 OPT_ADAMW, OPT_SGD, OPT_ADAMAX, OPT_ADADELTA = 0, 1, 2, 3
@@ -193,6 +194,33 @@ def lib():
                                         vp, i64, vp]
     L.fsdp_mx4_matmul.restype = ctypes.c_int
     L.fsdp_mx4_matmul.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, vp, i64, vp]
+    L.fsdp_fp8_quantize.restype = ctypes.c_int
+    L.fsdp_fp8_quantize.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp, vp, vp, vp]
+    L.fsdp_fp8_gather.restype = ctypes.c_int
+    L.fsdp_fp8_gather.argtypes = [vpp, vpp, i32, i64, i32, vp, vp]
+    L.fsdp_fp8_gather_packed.restype = ctypes.c_int
+    L.fsdp_fp8_gather_packed.argtypes = [vpp, vpp, i32, i64, vp, vp, vp]
+    L.fsdp_fp8_matmul_workspace.restype = i64
+    L.fsdp_fp8_matmul_workspace.argtypes = [i64, i64, i64]
+    L.fsdp_fp8_matmul.restype = ctypes.c_int
+    L.fsdp_fp8_matmul.argtypes = [vp, vp, i32, vp, vp, i32, i64, i64, i64, i32, vp, i64, vp, i64, vp]
+    L.fsdp_fp8_linear_workspace.restype = i64
+    L.fsdp_fp8_linear_workspace.argtypes = [i64, i64, i64]
+    L.fsdp_fp8_linear.restype = ctypes.c_int
+    L.fsdp_fp8_linear.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, i64, i32, vp, i64, vp, i64, vp]
+    L.fsdp_fp8_linear_grads_workspace.restype = i64
+    L.fsdp_fp8_linear_grads_workspace.argtypes = [i64, i64, i64, i32, i32]
+    L.fsdp_fp8_linear_grads.restype = ctypes.c_int
+    L.fsdp_fp8_linear_grads.argtypes = [vp, i32, i64, vp, i32, i64, i64, i64, i64, vp, vp, i32, i32, vp, i64, i32, vp,
+                                        i64, vp, i64, vp]
+    L.fsdp_rms_norm_fp8.restype = ctypes.c_int
+    L.fsdp_rms_norm_fp8.argtypes = [vp, i32, i64, vp, i32, i64, i64, i64, vp, i32, f64, vp, i64, i32, vp, i64, vp, vp,
+                                    vp, vp]
+    L.fsdp_rms_norm_grads_workspace.restype = i64
+    L.fsdp_rms_norm_grads_workspace.argtypes = [i64, i64, i32]
+    L.fsdp_rms_norm_grads.restype = ctypes.c_int
+    L.fsdp_rms_norm_grads.argtypes = [vp, i32, i64, vp, i32, i64, i64, i64, vp, i32, vp, vp, i64, vp, i64, i32, vp, vp,
+                                      i64, vp]
     L.fsdp_unshard_gather.restype = ctypes.c_int
     L.fsdp_unshard_gather.argtypes = [vpp, i32, i64, ctypes.c_int, vp, vp]
     L.fsdp_unflatten_views.restype = ctypes.c_int
