@@ -46,7 +46,29 @@ struct Fp8Product {
     int64_t ldo;
     int cus;
     void* stream;
+    float* parts;                     // fp8_parts_bytes(m, n, nb, cus) bytes, or null where that is 0
 };
 hipError_t launch_fp8_matmul(const Fp8Product& p);
+hipError_t launch_fp8_two(const Fp8Product& a, const Fp8Product& b);   // both, in one launch where neither has few rows
+// Bytes of a product's partial sums, a multiple of 16: 0 where its sum is not split.
+int64_t fp8_parts_bytes(int64_t m, int64_t n, int64_t nb, int cus);
+
+constexpr int kFp8Few = 16;                              // most tokens of launch_fp8_few
+// The product for a few tokens: x as it is, or in blocks (sx not null).
+struct Fp8Few {
+    const void* x;                 // [m][k] of xdt, ldx elements from row to row; or codes [m][nb * 128]
+    const uint8_t* sx;             // scales [m >> tx][nb], or null
+    int xdt, tx;
+    int64_t m, k, ldx;
+    const uint8_t *w, *sw;         // codes and scales of W [n][k]
+    int tw;
+    int64_t n, nb;
+    int dt;
+    void* out;                     // [m][n], ldo elements from row to row
+    int64_t ldo;
+    int cus;
+    void* stream;
+};
+hipError_t launch_fp8_few(const Fp8Few& p);
 
 }  // namespace fsdp

@@ -60,6 +60,16 @@ int64_t blocked_bytes(int64_t rows, int64_t cols) {
     return (rows * fp8_blocks(cols) * (kFp8Block + 1) + 15) / 16 * 16;
 }
 
+// Whether a linear product quantises x on the way (fsdp_fp8_few.hip).  Every workgroup
+// then does; a launch of its own costs 2 us (us, on the way and apart: one token, 28672 x
+// 8192 43.4 and 47, 8192 x 8192 17.1 and 19.7, 5120 x 1280 4.4 and 6.0; 4 tokens, 28672 x
+// 8192 53.5 and 57.8; 16 tokens, 2048 x 512 (64 blocks) 4.2 and 5.1, but 1000 x 1000 (128)
+// 5.7 and 5.3, 5120 x 1280 (160) 7.0 and 6.6).
+bool linear_few(int64_t m, int64_t k) {
+    const int64_t blocks = m * fp8_blocks(k);
+    return (m <= 4 && blocks <= 256) || (m <= kFp8Few && blocks <= 64);
+}
+
 }  // namespace
 
 extern "C" {
@@ -176,7 +186,7 @@ int fsdp_fp8_gather_packed(const void* const* codes, const void* const* scales, 
 int64_t fsdp_fp8_matmul_workspace(int64_t m, int64_t n, int64_t k) {
     if (check_product("fsdp_fp8_matmul_workspace", m, n, k)) return -1;
     ok();
-    return 0;
+    return fp8_parts_bytes(m, n, fp8_blocks(k), cu_count());
 }
 
 int fsdp_fp8_matmul(const void* a_codes, const void* a_scales, int32_t a_tile, const void* b_codes,
@@ -193,12 +203,14 @@ int fsdp_fp8_matmul(const void* a_codes, const void* a_scales, int32_t a_tile, c
         rc = check_rows(fn, "out", out, out_dt, m, n, ldo, true, r, outs);
         if (!rc) rc = check_blocked(fn, "a", a_codes, a_scales, a_tile, m, k, ins);
         if (!rc) rc = check_blocked(fn, "b", b_codes, b_scales, b_tile, n, k, ins);
-        if (!rc) rc = check_space(fn, workspace, workspace_bytes, 0, outs);
+        const int cus = cu_count();
+        const int64_t parts = fp8_parts_bytes(m, n, fp8_blocks(k), cus);
+        if (!rc) rc = check_space(fn, workspace, workspace_bytes, parts, outs);
         if (rc) return rc;
         if (!apart(outs, ins)) return fail(FSDP_E_ALIAS, "%s: out or the workspace overlaps another buffer", fn);
         const Fp8Product p{(const uint8_t*)a_codes, (const uint8_t*)a_scales, (const uint8_t*)b_codes,
                            (const uint8_t*)b_scales, shift(a_tile), shift(b_tile), m, n, fp8_blocks(k), (int)out_dt,
-                           out, r.ld, cu_count(), stream};
+                           out, r.ld, cus, stream, parts > 0 ? (float*)workspace : nullptr};
         (void)hipGetLastError();
         hipError_t e = launch_fp8_matmul(p);
         if (e != hipSuccess) return hip_fail(e, "product launch");
@@ -209,7 +221,7 @@ int fsdp_fp8_matmul(const void* a_codes, const void* a_scales, int32_t a_tile, c
 int64_t fsdp_fp8_linear_workspace(int64_t m, int64_t n, int64_t k) {
     if (check_product("fsdp_fp8_linear_workspace", m, n, k)) return -1;
     ok();
-    return blocked_bytes(m, k);
+    return linear_few(m, k) ? 0 : blocked_bytes(m, k) + fp8_parts_bytes(m, n, fp8_blocks(k), cu_count());
 }
 
 int fsdp_fp8_linear(const void* x, fsdp_dtype x_dt, int64_t m, int64_t k, int64_t ldx, const void* w_codes,
@@ -227,17 +239,26 @@ int fsdp_fp8_linear(const void* x, fsdp_dtype x_dt, int64_t m, int64_t k, int64_
         rc = check_rows(fn, "x", x, x_dt, m, k, ldx, k > 0, xr, ins);
         if (!rc) rc = check_rows(fn, "out", out, out_dt, m, n, ldo, true, yr, outs);
         if (!rc) rc = check_blocked(fn, "w", w_codes, w_scales, w_tile, n, k, ins);
-        if (!rc) rc = check_space(fn, workspace, workspace_bytes, blocked_bytes(m, k), outs);
+        const bool few = linear_few(m, k);
+        const int cus = cu_count();
+        const int64_t blocked = few ? 0 : blocked_bytes(m, k), parts = few ? 0 : fp8_parts_bytes(m, n, fp8_blocks(k), cus);
+        if (!rc) rc = check_space(fn, workspace, workspace_bytes, blocked + parts, outs);
         if (rc) return rc;
         if (!apart(outs, ins)) return fail(FSDP_E_ALIAS, "%s: an output or the workspace overlaps another buffer", fn);
         const int64_t nb = fp8_blocks(k);
-        uint8_t *c = (uint8_t*)workspace, *s = c + m * nb * kFp8Block;
         (void)hipGetLastError();
         hipError_t e = hipSuccess;
-        if (nb > 0) e = launch_fp8_quantize(Fp8Quant{x, (int)x_dt, m, k, xr.ld, 0, c, s, nullptr, nullptr}, nullptr, stream);
-        if (e == hipSuccess)
-            e = launch_fp8_matmul(Fp8Product{c, s, (const uint8_t*)w_codes, (const uint8_t*)w_scales, 0, shift(w_tile), m,
-                                             n, nb, (int)out_dt, out, yr.ld, cu_count(), stream});
+        if (few) {
+            e = launch_fp8_few(Fp8Few{x, nullptr, (int)x_dt, 0, m, k, xr.ld, (const uint8_t*)w_codes, (const uint8_t*)w_scales,
+                                      shift(w_tile), n, nb, (int)out_dt, out, yr.ld, cus, stream});
+        } else {
+            uint8_t *c = (uint8_t*)workspace, *s = c + m * nb * kFp8Block;
+            if (nb > 0) e = launch_fp8_quantize(Fp8Quant{x, (int)x_dt, m, k, xr.ld, 0, c, s, nullptr, nullptr}, nullptr, stream);
+            if (e == hipSuccess)
+                e = launch_fp8_matmul(Fp8Product{c, s, (const uint8_t*)w_codes, (const uint8_t*)w_scales, 0, shift(w_tile), m,
+                                                 n, nb, (int)out_dt, out, yr.ld, cus, stream,
+                                                 parts > 0 ? (float*)(c + blocked) : nullptr});
+        }
         if (e != hipSuccess) return hip_fail(e, "linear launch");
         return ok();
     });
@@ -258,14 +279,30 @@ static int check_grads(const char* fn, int64_t m, int64_t n, int64_t k, bool dx,
     return rc;
 }
 
-static int64_t grads_bytes(int64_t m, int64_t n, int64_t k, bool dx, bool dw) {
-    return (dx ? blocked_bytes(m, n) : 0) + (dw ? blocked_bytes(n, m) + blocked_bytes(k, m) : 0);
+// What the workspace holds: dy's blocks, dy's and x's along the tokens, partial sums of each product.
+struct GradSpace {
+    int64_t dy, dy_t, x_t, dx_parts, dw_parts, bytes;
+};
+static GradSpace grad_space(int64_t m, int64_t n, int64_t k, bool dx, bool dw) {
+    const int cus = cu_count();
+    GradSpace g{};
+    if (dx) {
+        g.dy = blocked_bytes(m, n);
+        g.dx_parts = fp8_parts_bytes(m, k, fp8_blocks(n), cus);
+    }
+    if (dw) {
+        g.dy_t = blocked_bytes(n, m);
+        g.x_t = blocked_bytes(k, m);
+        g.dw_parts = fp8_parts_bytes(n, k, fp8_blocks(m), cus);
+    }
+    g.bytes = g.dy + g.dy_t + g.x_t + g.dx_parts + g.dw_parts;
+    return g;
 }
 
 int64_t fsdp_fp8_linear_grads_workspace(int64_t m, int64_t n, int64_t k, int32_t want_dx, int32_t want_dw) {
     if (check_grads("fsdp_fp8_linear_grads_workspace", m, n, k, want_dx, want_dw)) return -1;
     ok();
-    return grads_bytes(m, n, k, want_dx, want_dw);
+    return grad_space(m, n, k, want_dx, want_dw).bytes;
 }
 
 int fsdp_fp8_linear_grads(const void* dy, fsdp_dtype dy_dt, int64_t lddy, const void* x, fsdp_dtype x_dt, int64_t ldx,
@@ -289,23 +326,21 @@ int fsdp_fp8_linear_grads(const void* dy, fsdp_dtype dy_dt, int64_t lddy, const 
         if (!rc && want_dx) rc = check_rows(fn, "dx", dx, dx_dt, m, k, lddx, true, dxr, outs);
         if (!rc && want_dw) rc = check_rows(fn, "dw", dw, dw_dt, n, k, lddw, true, dwr, outs);
         if (!rc && want_dx) rc = check_blocked(fn, "wt", wt_codes, wt_scales, wt_tile, k, n, ins);
-        if (!rc) rc = check_space(fn, workspace, workspace_bytes, grads_bytes(m, n, k, want_dx, want_dw), outs);
+        const GradSpace g = grad_space(m, n, k, want_dx, want_dw);
+        if (!rc) rc = check_space(fn, workspace, workspace_bytes, g.bytes, outs);
         if (rc) return rc;
         if (!apart(outs, ins)) return fail(FSDP_E_ALIAS, "%s: an output or the workspace overlaps another buffer", fn);
         const int64_t nbn = fp8_blocks(n), nbm = fp8_blocks(m);
         uint8_t* at = (uint8_t*)workspace;
-        uint8_t *q = nullptr, *sq = nullptr, *qt = nullptr, *st = nullptr, *xt = nullptr, *sx = nullptr;
-        if (want_dx) {
-            q = at;
-            sq = q + m * nbn * kFp8Block;
-            at += blocked_bytes(m, n);
-        }
-        if (want_dw) {
-            qt = at;
-            st = qt + n * nbm * kFp8Block;
-            xt = at + blocked_bytes(n, m);
-            sx = xt + k * nbm * kFp8Block;
-        }
+        auto take = [&](int64_t bytes) {
+            uint8_t* p = bytes > 0 ? at : nullptr;
+            at += bytes;
+            return p;
+        };
+        uint8_t *q = take(g.dy), *qt = take(g.dy_t), *xt = take(g.x_t);
+        float *dxp = (float*)take(g.dx_parts), *dwp = (float*)take(g.dw_parts);
+        uint8_t *sq = q ? q + m * nbn * kFp8Block : nullptr, *st = qt ? qt + n * nbm * kFp8Block : nullptr,
+                *sx = xt ? xt + k * nbm * kFp8Block : nullptr;
         const int cus = cu_count();
         hipError_t e = hipSuccess;
         (void)hipGetLastError();
@@ -314,11 +349,11 @@ int fsdp_fp8_linear_grads(const void* dy, fsdp_dtype dy_dt, int64_t lddy, const 
         const bool once = want_dw && m > 0 && n > 0 && dy_dt == x_dt;    // both operands in one launch
         if (m > 0 && n > 0) e = launch_fp8_quantize(of_dy, once ? &of_x : nullptr, stream);
         if (e == hipSuccess && want_dw && m > 0 && !once) e = launch_fp8_quantize(of_x, nullptr, stream);
-        if (e == hipSuccess && want_dx)
-            e = launch_fp8_matmul(Fp8Product{q, sq, (const uint8_t*)wt_codes, (const uint8_t*)wt_scales, 0, shift(wt_tile),
-                                             m, k, nbn, (int)dx_dt, dx, dxr.ld, cus, stream});
-        if (e == hipSuccess && want_dw)
-            e = launch_fp8_matmul(Fp8Product{qt, st, xt, sx, 0, 0, n, k, nbm, (int)dw_dt, dw, dwr.ld, cus, stream});
+        const Fp8Product of_dx{q, sq, (const uint8_t*)wt_codes, (const uint8_t*)wt_scales, 0, shift(wt_tile), m, k, nbn,
+                               (int)dx_dt, dx, dxr.ld, cus, stream, dxp};
+        const Fp8Product of_dw{qt, st, xt, sx, 0, 0, n, k, nbm, (int)dw_dt, dw, dwr.ld, cus, stream, dwp};
+        if (e == hipSuccess && want_dx && want_dw) e = launch_fp8_two(of_dx, of_dw);
+        else if (e == hipSuccess) e = launch_fp8_matmul(want_dx ? of_dx : of_dw);
         if (e != hipSuccess) return hip_fail(e, "linear launch");
         return ok();
     });

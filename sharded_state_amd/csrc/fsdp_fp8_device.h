@@ -53,4 +53,11 @@ __device__ __forceinline__ u32x2 fp8_codes8(const Raw8<F>& x, uint32_t s) {
     return s == 255 ? u32x2{0, 0} : u32x2{__builtin_bit_cast(uint32_t, w[0]), __builtin_bit_cast(uint32_t, w[1])};
 }
 
+// Two values rounded to a 16-bit format side by side, the first in the low half.
+template <int F>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+    if constexpr (F == FSDP_BF16) return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)x, (__bf16)y});
+    else return __builtin_bit_cast(uint32_t, f16x2{(_Float16)x, (_Float16)y});
+}
+
 }  // namespace fsdp
