@@ -589,12 +589,13 @@ FSDP_API int fsdp_fp8_linear_grads(const void* dy, fsdp_dtype dy_dt, int64_t ldd
  * it and 8-bit blocks behind it:
  *   h    = x + residual, an fp32 sum rounded to h_dt; x as it is without a residual
  *   rstd = 1 / sqrt(sum of h^2 / d + eps), sums in 64 bits
- *   y    = (h * rstd) * weight in fp32, quantised along d as fsdp_fp8_quantize
- *          does it, and where y is not NULL stored, rounded to y_dt
+ *   y    = h * rstd * weight, rounded once to fp32, quantised along d as
+ *          fsdp_fp8_quantize does it, and where y is not NULL stored in y_dt
  * x [m][d] of x_dt, residual and h [m][d] of h_dt (h is NULL exactly where
  * residual is; h may be the residual itself, or x where their types are one),
  * weight [d] of w_dt, rstd [m] or NULL; ld elements from row to row, any
- * alignment.  eps is finite and not negative.  d is at most FSDP_RMS_MAX_D. */
+ * alignment.  eps is finite and not negative; with eps = 0 a row of zeros has
+ * an infinite rstd and NaN for its norm.  d is at most FSDP_RMS_MAX_D. */
 FSDP_API int fsdp_rms_norm_fp8(const void* x, fsdp_dtype x_dt, int64_t ldx, const void* residual,
                                fsdp_dtype h_dt, int64_t ldr, int64_t m, int64_t d, const void* weight,
                                fsdp_dtype w_dt, double eps, void* h, int64_t ldh, fsdp_dtype y_dt, void* y,

@@ -1,5 +1,5 @@
 // fsdp_rms.h -- internal interface between the host layer of the norms over
-// features (fsdp_rms_abi.cpp) and their kernels (fsdp_rms.hip).  Not installed.
+// features (fsdp_rms_abi.cpp) and their kernels (fsdp_rms.hip, fsdp_rms_grads.hip).  Not installed.
 #pragma once
 
 #include <hip/hip_runtime.h>
