@@ -41,7 +41,7 @@ class Fp8:
     scales  uint8 [rows, ceil(cols / 128)], contiguous; with `tile`, one for each
             128 x 128 elements, [ceil(rows / 128), ceil(cols / 128)]"""
 
-    __slots__ = ("codes", "scales", "rows", "cols", "tile")
+    __slots__ = ("_codes", "_scales", "_both", "_at", "rows", "cols", "tile", "device")
 
     def __init__(self, codes, scales, cols, tile=False):
         nb = _blocks(cols)
@@ -55,20 +55,42 @@ class Fp8:
             raise ValueError("codes is on %s, scales on %s" % (codes.device, scales.device))
         if codes.data_ptr() % 16:
             raise ValueError("codes must be 16-byte aligned")
-        self.codes, self.scales, self.rows, self.cols, self.tile = codes, scales, rows, int(cols), bool(tile)
+        self._codes, self._scales, self._both, self._at = codes, scales, None, None
+        self.rows, self.cols, self.tile, self.device = rows, int(cols), bool(tile), codes.device
 
     @classmethod
     def empty(cls, rows, cols, device="cuda", tile=False):
-        nb = _blocks(cols)
+        """Not filled: one allocation, the scales behind the codes."""
         self = object.__new__(cls)               # what is allocated here needs no check
-        self.codes = torch.empty((rows, nb * BLOCK), dtype=torch.uint8, device=device)
-        self.scales = torch.empty((_blocks(rows) if tile else rows, nb), dtype=torch.uint8, device=device)
-        self.rows, self.cols, self.tile = rows, cols, bool(tile)
+        nb = _blocks(cols)
+        behind = rows * nb * BLOCK
+        self._both = both = torch.empty(behind + (_blocks(rows) if tile else rows) * nb, dtype=torch.uint8, device=device)
+        at = both.data_ptr()
+        self._codes, self._scales, self._at = None, None, (at, at + behind)
+        self.rows, self.cols, self.tile, self.device = rows, cols, bool(tile), both.device
         return self
 
+    def _views(self):
+        nb = _blocks(self.cols)
+        behind = self.rows * nb * BLOCK
+        self._codes = self._both[:behind].view(self.rows, nb * BLOCK)
+        self._scales = self._both[behind:].view(_blocks(self.rows) if self.tile else self.rows, nb)
+
     @property
-    def device(self):
-        return self.codes.device
+    def codes(self):
+        if self._codes is None:
+            self._views()
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._views()
+        return self._scales
+
+    def _ptrs(self):
+        """The addresses of codes and scales."""
+        return self._at or (self._codes.data_ptr(), self._scales.data_ptr())
 
     @property
     def shape(self):
@@ -80,6 +102,8 @@ class Fp8:
 
 def _target(out, rows, cols, tile, device, stream, name):
     if out is None:
+        if stream is None:
+            return Fp8.empty(rows, cols, device, tile)
         with _on(stream):
             return Fp8.empty(rows, cols, device, tile)
     if not isinstance(out, Fp8):
@@ -92,7 +116,7 @@ def _target(out, rows, cols, tile, device, stream, name):
 def _operand(t, name):
     if not isinstance(t, Fp8):
         raise TypeError("%s must be an Fp8" % name)
-    if not t.codes.is_cuda:
+    if t.device.type != "cuda":
         raise ValueError("%s must be on a device, got %s" % (name, t.device))
     return t
 
@@ -114,10 +138,10 @@ def fsdp_fp8_quantize(src, out=None, out_t=None, form="rows", tile=False, stream
     p = [None, None, None, None]
     if form != "columns":
         a = _target(out, rows, cols, tile, device, stream, "out")
-        p[0], p[1] = a.codes.data_ptr(), a.scales.data_ptr()
+        p[0], p[1] = a._ptrs()
     if form != "rows":
         t = _target(out_t, cols, rows, tile, device, stream, "out_t")
-        p[2], p[3] = t.codes.data_ptr(), t.scales.data_ptr()
+        p[2], p[3] = t._ptrs()
     _issue("fsdp_fp8_quantize", device, stream, src.data_ptr(), dt, rows, cols, ld, int(tile), *p)
     return a if form == "rows" else t if form == "columns" else (a, t)
 
@@ -130,7 +154,7 @@ def _shards(shards):
     for q, s in enumerate(shards):
         if not isinstance(s, Fp8) or s.rows != 1 or s.cols != S:
             raise ValueError("shards[%d] must be an Fp8 of one row and %d columns" % (q, S))
-        _dev(s.codes, "shards[%d]" % q)
+        _operand(s, "shards[%d]" % q)
     return shards, len(shards), S, shards[0].device
 
 
@@ -144,9 +168,9 @@ def fsdp_fp8_gather(shards, full=None, dtype=torch.bfloat16, stream=None):
     _dev(full, "full")
     if full.numel() != world * S:
         raise ValueError("full must hold world*shard = %d elements" % (world * S))
-    _one_device(device, full, *(s.codes for s in shards))
-    _issue("fsdp_fp8_gather", device, stream, ptr_array([s.codes.data_ptr() for s in shards]),
-           ptr_array([s.scales.data_ptr() for s in shards]), world, S, dtype_code(full.dtype), full.data_ptr())
+    _one_device(device, full, *shards)
+    codes, scales = zip(*(s._ptrs() for s in shards))
+    _issue("fsdp_fp8_gather", device, stream, ptr_array(codes), ptr_array(scales), world, S, dtype_code(full.dtype), full.data_ptr())
     return full
 
 
@@ -157,9 +181,9 @@ def fsdp_fp8_gather_packed(shards, full=None, stream=None):
     if S % BLOCK:
         raise ValueError("the shard's size %d is not a multiple of %d: the shards' blocks do not join" % (S, BLOCK))
     full = _target(full, 1, world * S, False, device, stream, "full")
-    _one_device(device, full.codes, *(s.codes for s in shards))
-    _issue("fsdp_fp8_gather_packed", device, stream, ptr_array([s.codes.data_ptr() for s in shards]),
-           ptr_array([s.scales.data_ptr() for s in shards]), world, S, full.codes.data_ptr(), full.scales.data_ptr())
+    _one_device(device, *shards)
+    codes, scales = zip(*(s._ptrs() for s in shards))
+    _issue("fsdp_fp8_gather_packed", device, stream, ptr_array(codes), ptr_array(scales), world, S, *full._ptrs())
     return full
 
 
@@ -196,10 +220,10 @@ def fsdp_fp8_matmul(a, b, out=None, dtype=torch.bfloat16, stream=None):
         raise ValueError("a has %d columns, b %d" % (a.cols, b.cols))
     m, n, k, device = a.rows, b.rows, a.cols, a.device
     out, ldo = _result(out, m, n, dtype, device, stream)
-    _one_device(device, b.codes, out)
+    _one_device(device, b, out)
     keep, space, nbytes = _space(N.lib().fsdp_fp8_matmul_workspace(m, n, k), device, stream)
-    _issue("fsdp_fp8_matmul", device, stream, a.codes.data_ptr(), a.scales.data_ptr(), int(a.tile), b.codes.data_ptr(),
-           b.scales.data_ptr(), int(b.tile), m, n, k, dtype_code(out.dtype), out.data_ptr(), ldo, space, nbytes)
+    _issue("fsdp_fp8_matmul", device, stream, *a._ptrs(), int(a.tile), *b._ptrs(),
+           int(b.tile), m, n, k, dtype_code(out.dtype), out.data_ptr(), ldo, space, nbytes)
     return out
 
 
@@ -222,10 +246,10 @@ def fsdp_fp8_linear(x, w, out=None, dtype=None, stream=None):
     m, k, ldx = _matrix(x, "x")
     n, device = w.rows, x.device
     out, ldo = _result(out, m, n, dtype or x.dtype, device, stream)
-    _one_device(device, w.codes, out)
+    _one_device(device, w, out)
     keep, space, nbytes = _space(N.lib().fsdp_fp8_linear_workspace(m, n, k), device, stream)
-    _issue("fsdp_fp8_linear", device, stream, x.data_ptr(), dtype_code(x.dtype), m, k, ldx, w.codes.data_ptr(),
-           w.scales.data_ptr(), int(w.tile), n, dtype_code(out.dtype), out.data_ptr(), ldo, space, nbytes)
+    _issue("fsdp_fp8_linear", device, stream, x.data_ptr(), dtype_code(x.dtype), m, k, ldx, *w._ptrs(),
+           int(w.tile), n, dtype_code(out.dtype), out.data_ptr(), ldo, space, nbytes)
     return out
 
 
@@ -248,7 +272,7 @@ def fsdp_fp8_linear_grads(dy, x, wt, dx=None, dw=None, dw_dtype=None, stream=Non
     want_dx, want_dw = dx is not False, dw is not False
     pdx = pdw = None
     lddx = lddw = cdx = cdw = 0
-    _one_device(device, x, wt.codes)
+    _one_device(device, x, wt)
     if want_dx:
         dx, lddx = _result(dx, m, k, x.dtype, device, stream)
         _one_device(device, dx)
@@ -260,6 +284,6 @@ def fsdp_fp8_linear_grads(dy, x, wt, dx=None, dw=None, dw_dtype=None, stream=Non
     keep, space, nbytes = _space(N.lib().fsdp_fp8_linear_grads_workspace(m, n, k, int(want_dx), int(want_dw)), device,
                                  stream)
     _issue("fsdp_fp8_linear_grads", device, stream, dy.data_ptr(), dtype_code(dy.dtype), lddy, x.data_ptr(),
-           dtype_code(x.dtype), ldx, m, n, k, wt.codes.data_ptr(), wt.scales.data_ptr(), int(wt.tile), cdx, pdx, lddx,
+           dtype_code(x.dtype), ldx, m, n, k, *wt._ptrs(), int(wt.tile), cdx, pdx, lddx,
            cdw, pdw, lddw, space, nbytes)
     return dx if want_dx else None, dw if want_dw else None

@@ -23,10 +23,21 @@ they are the norm of, rstd (float32, one a row), and the normed rows as a tensor
 unless asked for)."""
 
 
-def _rows(t, name):
+def _rows(t, name, m=None, d=None):
+    """(rows, columns, row stride) of a matrix; of m x d where they are given."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError("%s must be a matrix" % name)
-    return _matrix(t, name)
+    r = _matrix(t, name)
+    if m is not None and r[:2] != (m, d):
+        raise ValueError("%s must be a matrix of %d x %d" % (name, m, d))
+    return r
+
+
+def _vector(n, dtype, device, stream):
+    if stream is None:
+        return torch.empty(n, dtype=dtype, device=device)
+    with _on(stream):
+        return torch.empty(n, dtype=dtype, device=device)
 
 
 def _features(t, name, d, device):
@@ -55,9 +66,7 @@ def fsdp_rms_norm_fp8(x, weight, residual=None, eps=1e-6, out=None, h=None, y=No
                          "detach it, and take the gradients from fsdp_rms_norm_grads")
     res, ldr, cr, ldh = None, 0, 0, 0
     if residual is not None:
-        if tuple(_rows(residual, "residual")[:2]) != (m, d):
-            raise ValueError("residual must be a matrix of %d x %d" % (m, d))
-        ldr = _matrix(residual, "residual")[2]
+        ldr = _rows(residual, "residual", m, d)[2]
         h, ldh = _result(h, m, d, residual.dtype, device, stream)
         if h.dtype != residual.dtype:
             raise TypeError("h dtype %s differs from the residual's %s" % (h.dtype, residual.dtype))
@@ -73,11 +82,10 @@ def fsdp_rms_norm_fp8(x, weight, residual=None, eps=1e-6, out=None, h=None, y=No
         py, cy = y.data_ptr(), dtype_code(y.dtype)
     else:
         y = None
-    with _on(stream):
-        rstd = torch.empty(m, dtype=torch.float32, device=device)
+    rstd = _vector(m, torch.float32, device, stream)
     _issue("fsdp_rms_norm_fp8", device, stream, x.data_ptr(), dtype_code(x.dtype), ldx, res, cr, ldr, m, d,
            weight.data_ptr(), dtype_code(weight.dtype), float(eps), h.data_ptr() if res is not None else None, ldh, cy,
-           py, ldy, out.codes.data_ptr(), out.scales.data_ptr(), rstd.data_ptr())
+           py, ldy, *out._ptrs(), rstd.data_ptr())
     return RmsNorm(out, x if residual is None else h, rstd, y)
 
 
@@ -89,9 +97,7 @@ def fsdp_rms_norm_grads(dy, h, weight, rstd, dh=None, dx=None, dw=None, dw_dtype
     or dw=False: not wanted, and None in its place."""
     m, d, lddy = _rows(dy, "dy")
     device = dy.device
-    if tuple(_rows(h, "h")[:2]) != (m, d):
-        raise ValueError("h must be a matrix of %d x %d" % (m, d))
-    ldh = _matrix(h, "h")[2]
+    ldh = _rows(h, "h", m, d)[2]
     _features(weight, "weight", d, device)
     _features(rstd, "rstd", m, device)
     if rstd.dtype != torch.float32:
@@ -100,12 +106,11 @@ def fsdp_rms_norm_grads(dy, h, weight, rstd, dh=None, dx=None, dw=None, dw_dtype
     want_dx, want_dw = dx is not False, dw is not False
     pe, lde = None, 0
     if dh is not None:
-        if tuple(_rows(dh, "dh")[:2]) != (m, d):
-            raise ValueError("dh must be a matrix of %d x %d" % (m, d))
+        lde = _rows(dh, "dh", m, d)[2]
         if dh.dtype != h.dtype:
             raise TypeError("dh dtype %s differs from h's %s" % (dh.dtype, h.dtype))
         _one_device(device, dh)
-        pe, lde = dh.data_ptr(), _matrix(dh, "dh")[2]
+        pe = dh.data_ptr()
     pdx = pdw = None
     lddx = cdw = 0
     if want_dx:
@@ -116,8 +121,7 @@ def fsdp_rms_norm_grads(dy, h, weight, rstd, dh=None, dx=None, dw=None, dw_dtype
         pdx = dx.data_ptr()
     if want_dw:
         if dw is None:
-            with _on(stream):
-                dw = torch.empty(d, dtype=dw_dtype or weight.dtype, device=device)
+            dw = _vector(d, dw_dtype or weight.dtype, device, stream)
         _features(dw, "dw", d, device)
         pdw, cdw = dw.data_ptr(), dtype_code(dw.dtype)
     keep, space, nbytes = _space(N.lib().fsdp_rms_norm_grads_workspace(m, d, int(want_dw)), device, stream)
