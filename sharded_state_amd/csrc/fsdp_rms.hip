@@ -90,7 +90,7 @@ __global__ __launch_bounds__(1024) void k_rms(RmsForward p) {
             if (p.y) any_store8<WHOLE>((char*)p.y + row * p.ldy * (p.ydt == FSDP_F32 ? 4 : 2), p.ydt, c, d, v[u]);
             const uint32_t s = fp8_scale_byte(max_of_16(a));
             if (c < nb * kFp8Block) {
-                st8(reinterpret_cast<u32x2*>(p.codes + row * nb * kFp8Block + c), fp8_codes8<FSDP_F32>(y, s));
+                *reinterpret_cast<u32x2*>(p.codes + row * nb * kFp8Block + c) = fp8_codes8<FSDP_F32>(y, s);
                 if (t % 16 == 0) p.scales[row * nb + c / kFp8Block] = (uint8_t)s;
             }
         }

@@ -60,9 +60,10 @@ __device__ __forceinline__ void any_row8(const void* row, int dt, int c, int d, 
     else row8<FSDP_BF16, WHOLE>(load_row8<FSDP_BF16, WHOLE>((const char*)row, c, d), c, d, v);
 }
 
-// 16-bit rows and codes are stored with the non-temporal hint (h, y and codes of 4096 x
-// 4096 bf16 27.5 -> 25.4 us, of 8192 x 1000 16.0 -> 13.2); a lane's two stores of fp32
-// take half a line each, and with it 8191 x 8192 went from 142 to 159.
+// 16-bit rows are stored with the non-temporal hint (the forward of 4096 x 4096 bf16 27.5
+// -> 25.4 us, of 8192 x 1000 16.0 -> 13.2); a lane's two stores of fp32 take half a line
+// each, and with it 8191 x 8192 went from 142 to 159.  Codes are not: the product behind
+// reads them (norm and product of 200 x 5120 x 5120 26.1 us, 27.8 with the hint).
 template <int F, bool WHOLE>
 __device__ __forceinline__ void store_row8(char* row, int c, int d, const float (&v)[8]) {
     if (WHOLE ? c < d : c + 8 <= d) {
