@@ -50,7 +50,7 @@ __global__ __launch_bounds__(1024) void k_rms_grads(RmsBackward p) {
 #pragma unroll
     for (int u = 0; u < U; ++u) any_row8<WHOLE>(p.weight, p.wdt, (u * T + t) * 8, d, w[u]);
     for (int64_t row = blockIdx.x; row < p.m; row += gridDim.x) {
-        const RmsRow<DF, HF, U> x = kAhead ? next : load(row);
+        RmsRow<DF, HF, U> x = kAhead ? next : load(row);
         if (kAhead && row + gridDim.x < p.m) next = load(row + gridDim.x);
         double q = 0.0;
 #pragma unroll
@@ -65,6 +65,14 @@ __global__ __launch_bounds__(1024) void k_rms_grads(RmsBackward p) {
             }
         }
         if (!p.dx) continue;
+        // dx may be dh, and a ragged row's last lanes load what others will store: not only
+        // dy and h, of which the sum was made, but dh too is here before the sum's barrier
+        if constexpr (!WHOLE) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < (HF == FSDP_F32 ? 8 : 4); ++k) asm volatile("" : "+v"(x.dh[u].w[k]));
+        }
         q = row_sum(q, part[turn]);
         turn ^= 1;
         const float f = (float)(q / (double)d * (double)x.r * (double)x.r);
