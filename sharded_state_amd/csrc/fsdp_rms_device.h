@@ -103,7 +103,7 @@ __device__ __forceinline__ double row_sum(double x, double* part) {
 inline int rms_units(int64_t d, int64_t one) { return d <= one ? 1 : (d <= 16384 ? 2 : 4); }
 inline int rms_lanes(int64_t d, int64_t one) {
     const int64_t each = 512 * rms_units(d, one);
-    return (int)((d + each - 1) / each * 64);
+    return d > 0 ? (int)((d + each - 1) / each * 64) : 64;
 }
 
 // Run L<A, B, U, WHOLE>::run(p, stream) for formats a and b and rows of p.d.
