@@ -589,8 +589,9 @@ FSDP_API int fsdp_fp8_linear_grads(const void* dy, fsdp_dtype dy_dt, int64_t ldd
  * it and 8-bit blocks behind it:
  *   h    = x + residual, an fp32 sum rounded to h_dt; x as it is without a residual
  *   rstd = 1 / sqrt(sum of h^2 / d + eps), sums in 64 bits
- *   y    = h * rstd * weight, rounded once to fp32, quantised along d as
- *          fsdp_fp8_quantize does it, and where y is not NULL stored in y_dt
+ *   y    = h * rstd * weight in 64 bits: rounded once to the codes of blocks
+ *          along d like fsdp_fp8_quantize's, and where y is not NULL rounded to
+ *          fp32 and stored in y_dt
  * x [m][d] of x_dt, residual and h [m][d] of h_dt (h is NULL exactly where
  * residual is; h may be the residual itself, or x where their types are one),
  * weight [d] of w_dt, rstd [m] or NULL; ld elements from row to row, any

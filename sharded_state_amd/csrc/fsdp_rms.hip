@@ -6,14 +6,23 @@
 // The memory bounds it: 5 bytes an element in bf16, 11 with a fp32 stream.  A row stays in
 // registers from its one read to its last use, and a workgroup that has more of them loads
 // the next before it sums this one.  The row's sum is held in 64 bits (a fp32 square
-// overflows above 1.8e19), and so is the product that is rounded to y, once: beside the
-// memory that costs nothing.  Measured: 8191 x 8192, bf16 on a fp32 stream, 139 us (5.3 TB/s);
-// 8192 x 8192 bf16 89 us (5.3); 1000 x 1600 fp16 5.6 us; one token of 1280 2.7 us.
+// overflows above 1.8e19), and so is the product, which is rounded to codes once: through
+// fp32 one code in 2^20 would come out as its neighbour, at a gain of 1 to 8% of the time.
+// Measured: 8191 x 8192, bf16 on a fp32 stream, 142 us (5.2 TB/s); 8192 x 8192 bf16 91 us
+// (5.2); 1000 x 1600 fp16 5.9 us; one token of 1280 2.7 us.
 #include "fsdp_rms_device.h"
 
 #pragma clang fp contract(off)
 
 namespace fsdp {
+
+// z cut off after 20 bits behind the leading one, the last of them set where that left
+// something out: rounded from there to a format of fewer bits, it is z rounded once.
+__device__ __forceinline__ uint32_t to_odd(double z) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, z);
+    const uint32_t hi = (uint32_t)(b >> 32) | ((uint32_t)b != 0);
+    return __float_as_uint((float)__builtin_bit_cast(double, (uint64_t)hi << 32));
+}
 
 template <int XF, int HF, int U>
 struct RmsIn {
@@ -77,17 +86,23 @@ __global__ __launch_bounds__(1024) void k_rms(RmsForward p) {
         for (int u = 0; u < U; ++u) {
             const int c = (u * T + t) * 8;
             if (!kAhead) any_row8<WHOLE>(p.weight, p.wdt, c, d, w[u]);
+            if (p.y) {
+                float y[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) asm volatile("" : "+v"(v[u][k]), "+v"(w[u][k]));
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = (float)((double)v[u][k] * r * (double)w[u][k]);
+                any_store8<WHOLE>((char*)p.y + row * p.ldy * (p.ydt == FSDP_F32 ? 4 : 2), p.ydt, c, d, y);
+            }
             Raw8<FSDP_F32> y;
             uint32_t a = 0;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                asm volatile("" : "+v"(v[u][k]));            // widened again, not kept wide
-                v[u][k] = (float)((double)v[u][k] * r * (double)w[u][k]);
-                if (c + k >= d) v[u][k] = 0.0f;              // not 0 * infinity
-                y.w[k] = __float_as_uint(v[u][k]);
+                asm volatile("" : "+v"(v[u][k]), "+v"(w[u][k]));    // widened here, not kept wide
+                y.w[k] = to_odd((double)v[u][k] * r * (double)w[u][k]);
+                if (c + k >= d) y.w[k] = 0;                  // not 0 * infinity
                 a = max(a, y.w[k] & 0x7fffffffu);
             }
-            if (p.y) any_store8<WHOLE>((char*)p.y + row * p.ldy * (p.ydt == FSDP_F32 ? 4 : 2), p.ydt, c, d, v[u]);
             const uint32_t s = fp8_scale_byte(max_of_16(a));
             if (c < nb * kFp8Block) {
                 *reinterpret_cast<u32x2*>(p.codes + row * nb * kFp8Block + c) = fp8_codes8<FSDP_F32>(y, s);
