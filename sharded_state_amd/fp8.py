@@ -41,7 +41,7 @@ class Fp8:
     scales  uint8 [rows, ceil(cols / 128)], contiguous; with `tile`, one for each
             128 x 128 elements, [ceil(rows / 128), ceil(cols / 128)]"""
 
-    __slots__ = ("_codes", "_scales", "_both", "_at", "rows", "cols", "tile", "device")
+    __slots__ = ("_codes", "_scales", "_both", "rows", "cols", "tile", "device")
 
     def __init__(self, codes, scales, cols, tile=False):
         nb = _blocks(cols)
@@ -55,7 +55,7 @@ class Fp8:
             raise ValueError("codes is on %s, scales on %s" % (codes.device, scales.device))
         if codes.data_ptr() % 16:
             raise ValueError("codes must be 16-byte aligned")
-        self._codes, self._scales, self._both, self._at = codes, scales, None, None
+        self._codes, self._scales, self._both = codes, scales, None
         self.rows, self.cols, self.tile, self.device = rows, int(cols), bool(tile), codes.device
 
     @classmethod
@@ -63,18 +63,20 @@ class Fp8:
         """Not filled: one allocation, the scales behind the codes."""
         self = object.__new__(cls)               # what is allocated here needs no check
         nb = _blocks(cols)
-        behind = rows * nb * BLOCK
-        self._both = both = torch.empty(behind + (_blocks(rows) if tile else rows) * nb, dtype=torch.uint8, device=device)
-        at = both.data_ptr()
-        self._codes, self._scales, self._at = None, None, (at, at + behind)
-        self.rows, self.cols, self.tile, self.device = rows, cols, bool(tile), both.device
+        n = rows * nb * BLOCK + (_blocks(rows) if tile else rows) * nb
+        self._codes, self._scales, self._both = None, None, torch.empty(n, dtype=torch.uint8, device=device)
+        self.rows, self.cols, self.tile, self.device = rows, cols, bool(tile), self._both.device
         return self
 
     def _views(self):
+        both = self._both
+        if both is None:                         # made meanwhile, by another thread
+            return
         nb = _blocks(self.cols)
         behind = self.rows * nb * BLOCK
-        self._codes = self._both[:behind].view(self.rows, nb * BLOCK)
-        self._scales = self._both[behind:].view(_blocks(self.rows) if self.tile else self.rows, nb)
+        self._scales = both[behind:].view(_blocks(self.rows) if self.tile else self.rows, nb)
+        self._codes = both[:behind].view(self.rows, nb * BLOCK)
+        self._both = None                        # from here on the views are the matrix, copied or pickled as such
 
     @property
     def codes(self):
@@ -90,7 +92,11 @@ class Fp8:
 
     def _ptrs(self):
         """The addresses of codes and scales."""
-        return self._at or (self._codes.data_ptr(), self._scales.data_ptr())
+        both = self._both
+        if both is None:
+            return self._codes.data_ptr(), self._scales.data_ptr()
+        at = both.data_ptr()
+        return at, at + self.rows * _blocks(self.cols) * BLOCK
 
     @property
     def shape(self):

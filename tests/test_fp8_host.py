@@ -1,7 +1,9 @@
 """8-bit blocks and the norm in front of them on the host: the tests' own
 reference against the format's numbers written out, argument validation of the C
 entry points (fake, never-dereferenced pointers) and of the binding."""
+import copy
 import ctypes
+import pickle
 
 import numpy as np
 import pytest
@@ -273,3 +275,19 @@ def test_views_of_a_packed_unit():
     assert v[5].codes.data_ptr() == full.codes.data_ptr() + 1664 and v[5].scales[0, 0] == 13
     with pytest.raises(ValueError):
         ss.fsdp_fp8_views(full, [(41, 128)])
+
+
+@pytest.mark.parametrize("tile", [False, True])
+def test_copies_have_memory_of_their_own(tile):
+    q = ss.Fp8.empty(130, 300, "cpu", tile)
+    q.codes.copy_(torch.arange(q.codes.numel()).view_as(q.codes) % 120)
+    q.scales.fill_(127)
+    for same in (copy.deepcopy(q), pickle.loads(pickle.dumps(q)), ss.Fp8(q.codes.clone(), q.scales.clone(), 300, tile)):
+        assert same.shape == (130, 300) and same.tile == tile and same.device == q.device
+        assert torch.equal(same.codes, q.codes) and torch.equal(same.scales, q.scales)
+        assert same._ptrs() == (same.codes.data_ptr(), same.scales.data_ptr())
+        assert not set(same._ptrs()) & set(q._ptrs())
+        same.codes.zero_()
+        assert q.codes.any()
+    fresh = copy.deepcopy(ss.Fp8.empty(3, 128, "cpu", tile))     # before anybody asked for its views
+    assert fresh._ptrs() == (fresh.codes.data_ptr(), fresh.scales.data_ptr())
