@@ -4,6 +4,7 @@
 
 #include "fsdp_fp8_device.h"
 #include "fsdp_mx4_tiles.h"    // tile_of and the vector types
+#include "fsdp_waits.h"
 
 #pragma clang fp contract(off)
 
@@ -263,30 +264,19 @@ __device__ __forceinline__ void fp8_products(const Fp8Jobs& j) {
         for (int f = 0; f < FN; ++f) sb[f] = (int)(sn[FM + f] >> ((kt & 2) * 8));
     };
     // The wait for a stage's loads, with those of `behind` stages behind it on their way.
-    auto arrived = [&](auto behind) {
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(decltype(behind)::value * kLoads) : "memory");
-    };
+    auto arrived = [&](auto behind) { wait_memory<decltype(behind)::value * kLoads>(); };
     // Accesses that went out behind the loads that the next stage 0 waits for: a tile's
     // stores, a fetch of scales.  They need not be over then.
     int newer = 0;
     constexpr int kStored = FM * FN * 2 < 62 - kRows ? FM * FN * 2 : 62 - kRows;    // least stores of a whole tile, a wave: 16 bits
-    // The same wait with `n` accesses behind them, 0, kRows, kStored or their sum, as
-    // one instruction to the compiler, which else would end a block here.
+    // The same wait with `n` accesses behind them, 0, kRows, kStored or their sum.
     auto arrived_behind = [&](int n) {
         if constexpr (NS > 2) {
             arrived(std::integral_constant<int, NS - 2>{});
         } else {
-            asm volatile("s_cmp_ge_i32 %0, %1\n\ts_cbranch_scc1 2f\n\ts_cmp_ge_i32 %0, %2\n\ts_cbranch_scc1 1f\n\t"
-                         "s_waitcnt vmcnt(%3)\n1:\n\ts_waitcnt vmcnt(%4)\n2:\n\ts_waitcnt vmcnt(%5)"
-                         ::"s"(__builtin_amdgcn_readfirstlane(n)), "n"(kStored), "n"(kRows), "n"(kBehind), "n"(kRows + kBehind), "n"(kStored + kBehind) : "memory", "scc");
+            wait_memory_by<kStored, kRows, kBehind, kRows + kBehind, kStored + kBehind>(n);
         }
     };
-    auto together = [&]() {
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-    };
-
     f32x16 acc[FM][FN];
     // Stage J of two, in `slot`, the fragments of its step 0 read already; `next`: the
     // slot of the stage behind it.
@@ -311,7 +301,7 @@ __device__ __forceinline__ void fp8_products(const Fp8Jobs& j) {
         if constexpr (J == 0) arrived_behind(newer);
         else arrived(std::integral_constant<int, NS - 2>{});
         behind_wait();
-        together();
+        meet_in_lds();
         behind_barrier();
 #pragma unroll
         for (int q = 0; q < kIns; ++q) {
@@ -333,7 +323,7 @@ __device__ __forceinline__ void fp8_products(const Fp8Jobs& j) {
         constexpr bool kWhole = decltype(whole_tile)::value;
         auto turned = [](int r) { return T::kOutRow == 128 ? r >> 1 & 7 : r >> 2 & 3; };
         int le = l;
-        asm volatile("" : "+v"(le));                         // what follows from it is not kept through the stages
+        unknown(le);                                         // what follows from it is not kept through the stages
         const int r = le & 31, hh = le >> 5;
         uint8_t* const mine = lds + T::kOut + w * 32 * T::kOutRow;
         uint8_t* const to = mine + r * T::kOutRow;
@@ -406,7 +396,7 @@ __device__ __forceinline__ void fp8_products(const Fp8Jobs& j) {
         }
         arrived(std::integral_constant<int, NS - 1>{});
         put_scales(scales, 0);
-        together();
+        meet_in_lds();
         read_scales(0, 0);
         take_scales(0);
 #pragma unroll
@@ -444,7 +434,7 @@ __device__ __forceinline__ void fp8_products(const Fp8Jobs& j) {
             stage(std::integral_constant<int, 1>{}, slot + 1, 2 * pair,
                   [&]() {
                       put_scales(scales, other);
-                      if (kAhead) asm volatile("" ::"v"(line));
+                      if (kAhead) needed(line);
                   },
                   [&]() { read_scales(half, then); });
             if (kAhead) line = ahead();
@@ -468,7 +458,7 @@ __device__ __forceinline__ void fp8_products(const Fp8Jobs& j) {
         else store(std::integral_constant<int, FSDP_BF16>{});
         newer = done.rows_a == BM && done.rows_b == BN ? kStored : 0;
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");         // loads into LDS end before the workgroup does
+    wait_memory<0>();                                        // loads into LDS end before the workgroup does
 }
 
 template <int BM, int BN, int WM, int WN, int NS>
