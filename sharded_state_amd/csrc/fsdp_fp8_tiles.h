@@ -266,7 +266,9 @@ __device__ __forceinline__ void fp8_products(const Fp8Jobs& j) {
     // The wait for a stage's loads, with those of `behind` stages behind it on their way.
     auto arrived = [&](auto behind) { wait_memory<decltype(behind)::value * kLoads>(); };
     // Accesses that went out behind the loads that the next stage 0 waits for: a tile's
-    // stores, a fetch of scales.  They need not be over then.
+    // stores, a fetch of scales.  They need not be over then.  With kAhead one more is there
+    // at every such wait, the first one's too: each pair's loads, and the first pair's
+    // before the loop, are followed by an access of ahead().
     int newer = 0;
     constexpr int kStored = FM * FN * 2 < 62 - kRows ? FM * FN * 2 : 62 - kRows;    // least stores of a whole tile, a wave: 16 bits
     // The same wait with `n` accesses behind them, 0, kRows, kStored or their sum.
@@ -277,6 +279,7 @@ __device__ __forceinline__ void fp8_products(const Fp8Jobs& j) {
             wait_memory_by<kStored, kRows, kBehind, kRows + kBehind, kStored + kBehind>(n);
         }
     };
+
     f32x16 acc[FM][FN];
     // Stage J of two, in `slot`, the fragments of its step 0 read already; `next`: the
     // slot of the stage behind it.
@@ -382,6 +385,7 @@ __device__ __forceinline__ void fp8_products(const Fp8Jobs& j) {
     };
 
     u32x4 scales[kRows];
+    uint32_t line = 0;                                       // of those brought ahead
     Fp8Tile at = ld;                                         // the tile that is being made
     int half = 0;                                            // where its 16 stages' scales lie
     if (at.nk > 0) {
@@ -395,6 +399,7 @@ __device__ __forceinline__ void fp8_products(const Fp8Jobs& j) {
             load_part(1, t + 1, 0, 1);
         }
         arrived(std::integral_constant<int, NS - 1>{});
+        if (kAhead) line = ahead();
         put_scales(scales, 0);
         meet_in_lds();
         read_scales(0, 0);
@@ -404,7 +409,6 @@ __device__ __forceinline__ void fp8_products(const Fp8Jobs& j) {
 #pragma unroll
         for (int x = 0; x < 2 * FM; ++x) read_a(0, 0, x / 2, x % 2);
     }
-    uint32_t line = 0;                                       // of those brought ahead
     int pair = 0;                                            // of the stream, modulo NS / 2
     for (uint32_t t = blockIdx.x; t < j.tiles; t += gridDim.x) {
 #pragma unroll
