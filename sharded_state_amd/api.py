@@ -51,6 +51,16 @@ def _issue(name, device, stream, *args):
         check(name, rc)
 
 
+def _changed(*given):
+    """Count a call's writes into the tensors that its caller gave for its results (what is no
+    tensor was not given), as torch's own in-place operations do: a graph that saved one of
+    them for its backward then refuses to run it on the new values.  Gathers do not count: the
+    backward gathers the values again that the forward's views of the full buffer had."""
+    given = [t for t in given if isinstance(t, torch.Tensor)]
+    if given:
+        torch.autograd.graph.increment_version(given)
+
+
 def _dev(t, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a tensor" % name)

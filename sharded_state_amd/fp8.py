@@ -24,7 +24,7 @@ import torch
 
 from . import _native as N
 from ._native import ptr_array
-from .api import _dev, _issue, _on, dtype_code
+from .api import _changed, _dev, _issue, _on, dtype_code
 from .mx4 import _matrix, _one_device, _result, _space
 
 BLOCK = 128
@@ -225,11 +225,13 @@ def fsdp_fp8_matmul(a, b, out=None, dtype=torch.bfloat16, stream=None):
     if a.cols != b.cols:
         raise ValueError("a has %d columns, b %d" % (a.cols, b.cols))
     m, n, k, device = a.rows, b.rows, a.cols, a.device
+    given = out
     out, ldo = _result(out, m, n, dtype, device, stream)
     _one_device(device, b, out)
     keep, space, nbytes = _space(N.lib().fsdp_fp8_matmul_workspace(m, n, k), device, stream)
     _issue("fsdp_fp8_matmul", device, stream, *a._ptrs(), int(a.tile), *b._ptrs(),
            int(b.tile), m, n, k, dtype_code(out.dtype), out.data_ptr(), ldo, space, nbytes)
+    _changed(given)
     return out
 
 
@@ -251,11 +253,13 @@ def fsdp_fp8_linear(x, w, out=None, dtype=None, stream=None):
                          "the gradients from fsdp_fp8_linear_grads")
     m, k, ldx = _matrix(x, "x")
     n, device = w.rows, x.device
+    given = out
     out, ldo = _result(out, m, n, dtype or x.dtype, device, stream)
     _one_device(device, w, out)
     keep, space, nbytes = _space(N.lib().fsdp_fp8_linear_workspace(m, n, k), device, stream)
     _issue("fsdp_fp8_linear", device, stream, x.data_ptr(), dtype_code(x.dtype), m, k, ldx, *w._ptrs(),
            int(w.tile), n, dtype_code(out.dtype), out.data_ptr(), ldo, space, nbytes)
+    _changed(given)
     return out
 
 
@@ -276,6 +280,7 @@ def fsdp_fp8_linear_grads(dy, x, wt, dx=None, dw=None, dw_dtype=None, stream=Non
         raise ValueError("dy has %d rows, x %d" % (m, mx))
     device = dy.device
     want_dx, want_dw = dx is not False, dw is not False
+    given = dx, dw
     pdx = pdw = None
     lddx = lddw = cdx = cdw = 0
     _one_device(device, x, wt)
@@ -292,4 +297,5 @@ def fsdp_fp8_linear_grads(dy, x, wt, dx=None, dw=None, dw_dtype=None, stream=Non
     _issue("fsdp_fp8_linear_grads", device, stream, dy.data_ptr(), dtype_code(dy.dtype), lddy, x.data_ptr(),
            dtype_code(x.dtype), ldx, m, n, k, *wt._ptrs(), int(wt.tile), cdx, pdx, lddx,
            cdw, pdw, lddw, space, nbytes)
+    _changed(*given)
     return dx if want_dx else None, dw if want_dw else None

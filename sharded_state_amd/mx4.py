@@ -21,7 +21,7 @@ import torch
 
 from . import _native as N
 from ._native import ptr_array
-from .api import _dev, _issue, _on, dtype_code
+from .api import _changed, _dev, _issue, _on, dtype_code
 
 BLOCK = 32
 
@@ -220,10 +220,12 @@ def fsdp_mx4_matmul(a, b, out=None, dtype=torch.bfloat16, stream=None):
     if a.cols != b.cols:
         raise ValueError("a has %d columns, b %d" % (a.cols, b.cols))
     device = a.device
+    given = out
     out, ldo = _result(out, a.rows, b.rows, dtype, device, stream)
     _one_device(device, b.codes, out)
     _issue("fsdp_mx4_matmul", device, stream, a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
            b.scales.data_ptr(), a.rows, b.rows, a.cols, dtype_code(out.dtype), out.data_ptr(), ldo)
+    _changed(given)
     return out
 
 
@@ -250,11 +252,13 @@ def fsdp_mx4_linear(x, w, out=None, stream=None):
                          "the gradients from fsdp_mx4_linear_grads")
     m, k, ldx = _matrix(x, "x")
     device = x.device
+    given = out
     out, ldo = _result(out, m, w.rows, x.dtype, device, stream)
     _one_device(device, w.codes, out)
     keep, space, nbytes = _space(N.lib().fsdp_mx4_linear_workspace(m, k), device, stream)
     _issue("fsdp_mx4_linear", device, stream, x.data_ptr(), dtype_code(x.dtype), m, k, ldx, w.codes.data_ptr(),
            w.scales.data_ptr(), w.rows, dtype_code(out.dtype), out.data_ptr(), ldo, space, nbytes)
+    _changed(given)
     return out
 
 
@@ -276,6 +280,7 @@ def fsdp_mx4_linear_grads(dy, x, wt, dx=None, dw=None, dw_dtype=None, stream=Non
         raise ValueError("dy has %d rows, x %d" % (m, mx))
     device = dy.device
     want_dx, want_dw = dx is not False, dw is not False
+    given = dx, dw
     pdx = pdw = None
     lddx = lddw = cdx = cdw = 0
     _one_device(device, x, wt.codes)
@@ -292,4 +297,5 @@ def fsdp_mx4_linear_grads(dy, x, wt, dx=None, dw=None, dw_dtype=None, stream=Non
     _issue("fsdp_mx4_linear_grads", device, stream, dy.data_ptr(), dtype_code(dy.dtype), lddy, x.data_ptr(),
            dtype_code(x.dtype), ldx, m, n, k, wt.codes.data_ptr(), wt.scales.data_ptr(), cdx, pdx, lddx, cdw, pdw,
            lddw, space, nbytes)
+    _changed(*given)
     return dx if want_dx else None, dw if want_dw else None

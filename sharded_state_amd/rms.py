@@ -6,14 +6,15 @@ residual's addition before it, 8-bit blocks behind it, and its gradients.
     dx, dw = ss.fsdp_rms_norm_grads(dy, o.h, weight, o.rstd, dh=dh)
 
 dx is the gradient of x and of the residual alike; dh is the gradient that the
-sum has from elsewhere, the residual path behind the layer.
+sum has from elsewhere, the residual path behind the layer.  A tensor given for a result
+counts as changed in place: a graph that saved it refuses its backward.
 """
 import collections
 
 import torch
 
 from . import _native as N
-from .api import _issue, _on, dtype_code
+from .api import _changed, _issue, _on, dtype_code
 from .fp8 import Fp8, _target
 from .mx4 import _matrix, _one_device, _result, _space
 
@@ -64,6 +65,7 @@ def fsdp_rms_norm_fp8(x, weight, residual=None, eps=1e-6, out=None, h=None, y=No
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, residual)):
         raise ValueError("an input requires grad, and the outputs would carry none: call under torch.no_grad() or "
                          "detach it, and take the gradients from fsdp_rms_norm_grads")
+    given = h, y
     res, ldr, cr, ldh = None, 0, 0, 0
     if residual is not None:
         ldr = _rows(residual, "residual", m, d)[2]
@@ -86,6 +88,7 @@ def fsdp_rms_norm_fp8(x, weight, residual=None, eps=1e-6, out=None, h=None, y=No
     _issue("fsdp_rms_norm_fp8", device, stream, x.data_ptr(), dtype_code(x.dtype), ldx, res, cr, ldr, m, d,
            weight.data_ptr(), dtype_code(weight.dtype), float(eps), h.data_ptr() if res is not None else None, ldh, cy,
            py, ldy, *out._ptrs(), rstd.data_ptr())
+    _changed(*given)
     return RmsNorm(out, x if residual is None else h, rstd, y)
 
 
@@ -104,6 +107,7 @@ def fsdp_rms_norm_grads(dy, h, weight, rstd, dh=None, dx=None, dw=None, dw_dtype
         raise TypeError("rstd must be float32, got %s" % rstd.dtype)
     _one_device(device, h)
     want_dx, want_dw = dx is not False, dw is not False
+    given = dx, dw
     pe, lde = None, 0
     if dh is not None:
         lde = _rows(dh, "dh", m, d)[2]
@@ -128,4 +132,5 @@ def fsdp_rms_norm_grads(dy, h, weight, rstd, dh=None, dx=None, dw=None, dw_dtype
     _issue("fsdp_rms_norm_grads", device, stream, dy.data_ptr(), dtype_code(dy.dtype), lddy, h.data_ptr(),
            dtype_code(h.dtype), ldh, m, d, weight.data_ptr(), dtype_code(weight.dtype), rstd.data_ptr(), pe, lde, pdx,
            lddx, cdw, pdw, space, nbytes)
+    _changed(*given)
     return dx if want_dx else None, dw if want_dw else None
