@@ -10,6 +10,7 @@ import contextlib
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _native as N
 from ._native import AdamWHP, OptimHP, Unit, View, check, i64_array, ptr_array
@@ -59,6 +60,18 @@ def _changed(*given):
     given = [t for t in given if isinstance(t, torch.Tensor)]
     if given:
         torch.autograd.graph.increment_version(given)
+
+
+def _no_tangents(*inputs):
+    """Refuse inputs with a forward-mode tangent, which a result would lose (what is no tensor
+    has none).  Grad mode has no say in these.  Outside every dual level there is nothing to
+    look for (0.7 us an input)."""
+    if getattr(forward_ad, "_current_level", 0) < 0:
+        return
+    for t in inputs:
+        if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError("an input has a forward-mode tangent, and the outputs would carry none: take the primal "
+                             "from torch.autograd.forward_ad.unpack_dual")
 
 
 def _dev(t, name):

@@ -24,7 +24,7 @@ import torch
 
 from . import _native as N
 from ._native import ptr_array
-from .api import _changed, _dev, _issue, _on, dtype_code
+from .api import _changed, _dev, _issue, _no_tangents, _on, dtype_code
 from .mx4 import _matrix, _one_device, _result, _space
 
 BLOCK = 128
@@ -240,7 +240,7 @@ def fsdp_fp8_linear(x, w, out=None, dtype=None, stream=None):
     is quantised along its features on the way, or an Fp8 (what
     ``fsdp_rms_norm_fp8`` gives).  y has `out`'s dtype, else `dtype`, else x's
     (bfloat16 for an Fp8), and no graph: where grad mode is on, an x that requires
-    grad is refused."""
+    grad is refused, and so is one with a forward-mode tangent."""
     _operand(w, "w")
     if isinstance(x, Fp8):
         if x.cols != w.cols:
@@ -251,6 +251,7 @@ def fsdp_fp8_linear(x, w, out=None, dtype=None, stream=None):
     if x.requires_grad and torch.is_grad_enabled():
         raise ValueError("x requires grad, and y would carry none: call under torch.no_grad() or detach x, and take "
                          "the gradients from fsdp_fp8_linear_grads")
+    _no_tangents(x)
     m, k, ldx = _matrix(x, "x")
     n, device = w.rows, x.device
     given = out
@@ -274,6 +275,7 @@ def fsdp_fp8_linear_grads(dy, x, wt, dx=None, dw=None, dw_dtype=None, stream=Non
     for name, t, c in (("dy", dy, wt.cols), ("x", x, wt.rows)):
         if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[1] != c:
             raise ValueError("%s must be a matrix of %d columns" % (name, c))
+    _no_tangents(dy, x)
     m, n, lddy = _matrix(dy, "dy")
     mx, k, ldx = _matrix(x, "x")
     if m != mx:

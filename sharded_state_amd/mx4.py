@@ -21,7 +21,7 @@ import torch
 
 from . import _native as N
 from ._native import ptr_array
-from .api import _changed, _dev, _issue, _on, dtype_code
+from .api import _changed, _dev, _issue, _no_tangents, _on, dtype_code
 
 BLOCK = 32
 
@@ -242,7 +242,7 @@ def fsdp_mx4_linear(x, w, out=None, stream=None):
     """y = x W^T for x [tokens, in] and W an Mx4 [out, in]: x is quantised along
     its features on the way (for a few tokens within the one launch).  y has x's
     dtype unless `out` says otherwise, and no graph: where grad mode is on, an x
-    that requires grad is refused."""
+    that requires grad is refused, and so is one with a forward-mode tangent."""
     if not isinstance(w, Mx4):
         raise TypeError("w must be an Mx4")
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != w.cols:
@@ -250,6 +250,7 @@ def fsdp_mx4_linear(x, w, out=None, stream=None):
     if x.requires_grad and torch.is_grad_enabled():
         raise ValueError("x requires grad, and y would carry none: call under torch.no_grad() or detach x, and take "
                          "the gradients from fsdp_mx4_linear_grads")
+    _no_tangents(x)
     m, k, ldx = _matrix(x, "x")
     device = x.device
     given = out
@@ -274,6 +275,7 @@ def fsdp_mx4_linear_grads(dy, x, wt, dx=None, dw=None, dw_dtype=None, stream=Non
     for name, t, c in (("dy", dy, wt.cols), ("x", x, wt.rows)):
         if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[1] != c:
             raise ValueError("%s must be a matrix of %d columns" % (name, c))
+    _no_tangents(dy, x)
     m, n, lddy = _matrix(dy, "dy")
     mx, k, ldx = _matrix(x, "x")
     if m != mx:

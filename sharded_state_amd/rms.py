@@ -14,7 +14,7 @@ import collections
 import torch
 
 from . import _native as N
-from .api import _changed, _issue, _on, dtype_code
+from .api import _changed, _issue, _no_tangents, _on, dtype_code
 from .fp8 import Fp8, _target
 from .mx4 import _matrix, _one_device, _result, _space
 
@@ -58,7 +58,9 @@ def fsdp_rms_norm_fp8(x, weight, residual=None, eps=1e-6, out=None, h=None, y=No
                  x of its dtype
     y            True, or a matrix: the normed rows as a tensor too (dtype of x for True)
 
-    No graph: where grad mode is on, an input that requires grad is refused."""
+    No graph: where grad mode is on, an input that requires grad is refused, and so is one with a
+    forward-mode tangent."""
+    _no_tangents(x, weight, residual)
     m, d, ldx = _rows(x, "x")
     device = x.device
     _features(weight, "weight", d, device)
@@ -98,6 +100,7 @@ def fsdp_rms_norm_grads(dy, h, weight, rstd, dh=None, dx=None, dw=None, dw_dtype
     and dw (dw_dtype, else the weight's dtype).  dx and dw may be given (dx may be
     dh, or a dy of h's dtype; dw: the weight's place in a flat gradient); dx=False
     or dw=False: not wanted, and None in its place."""
+    _no_tangents(dy, h, weight, rstd, dh)
     m, d, lddy = _rows(dy, "dy")
     device = dy.device
     ldh = _rows(h, "h", m, d)[2]
