@@ -17,11 +17,29 @@
 namespace fsdp {
 
 // z cut off after 20 bits behind the leading one, the last of them set where that left
-// something out: rounded from there to a format of fewer bits, it is z rounded once.
+// something out: rounded from there to a format of fewer bits, it is z rounded once, where
+// fp32 holds those 20 bits (z from 2^-129 to below 2^128).
 __device__ __forceinline__ uint32_t to_odd(double z) {
     const uint64_t b = __builtin_bit_cast(uint64_t, z);
     const uint32_t hi = (uint32_t)(b >> 32) | ((uint32_t)b != 0);
     return __float_as_uint((float)__builtin_bit_cast(double, (uint64_t)hi << 32));
+}
+
+// For a block with products that to_odd does not give: from 2^128 on, or with ties between
+// codes among fp32's subnormals.  y: the high halves of eight products of a lane, the last
+// bit set where the low half is not 0.  Gives the block's scale byte, and in y's place what
+// is left of the products divided by the scale, which fp32 holds or is far under a tie.
+__device__ __forceinline__ uint32_t far_scale(Raw8<FSDP_F32>& y) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a = max(a, y.w[k] & 0x7fffffffu);
+    a = max_of_16(a);
+    const int e = (int)(a >> 20) - 1023 + 127 - 8 + ((a & 0xfffffu) > 0xc0000u);     // as fp8_scale_byte
+    const uint32_t s = e > 254 ? 255u : (uint32_t)(e < 1 ? 1 : e);
+    const double f = __builtin_bit_cast(double, (uint64_t)(1023 + 127 - (int)s) << 52);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y.w[k] = __float_as_uint((float)(__builtin_bit_cast(double, (uint64_t)y.w[k] << 32) * f));
+    return s;
 }
 
 template <int XF, int HF, int U>
@@ -103,9 +121,21 @@ __global__ __launch_bounds__(1024) void k_rms(RmsForward p) {
                 if (c + k >= d) y.w[k] = 0;                  // not 0 * infinity
                 a = max(a, y.w[k] & 0x7fffffffu);
             }
-            const uint32_t s = fp8_scale_byte(max_of_16(a));
+            a = max_of_16(a);
+            uint32_t s = fp8_scale_byte(a), by = s;
+            // a tie is 2^(s - 137) at least, and to_odd needs 2^-129; zeros have none
+            if (s == 255 || (s < 8 && a != 0)) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    asm volatile("" : "+v"(v[u][k]), "+v"(w[u][k]));
+                    const uint64_t z = __builtin_bit_cast(uint64_t, (double)v[u][k] * r * (double)w[u][k]);
+                    y.w[k] = c + k < d ? (uint32_t)(z >> 32) | ((uint32_t)z != 0) : 0u;
+                }
+                s = far_scale(y);
+                by = s == 255 ? 255u : 127u;
+            }
             if (c < nb * kFp8Block) {
-                *reinterpret_cast<u32x2*>(p.codes + row * nb * kFp8Block + c) = fp8_codes8<FSDP_F32>(y, s);
+                *reinterpret_cast<u32x2*>(p.codes + row * nb * kFp8Block + c) = fp8_codes8<FSDP_F32>(y, by);
                 if (t % 16 == 0) p.scales[row * nb + c / kFp8Block] = (uint8_t)s;
             }
         }
