@@ -596,7 +596,8 @@ FSDP_API int fsdp_fp8_linear_grads(const void* dy, fsdp_dtype dy_dt, int64_t ldd
  * residual is; h may be the residual itself, or x where their types are one),
  * weight [d] of w_dt, rstd [m] or NULL; ld elements from row to row, any
  * alignment.  eps is finite and not negative; with eps = 0 a row of zeros has
- * an infinite rstd and NaN for its norm.  d is at most FSDP_RMS_MAX_D. */
+ * an infinite rstd and NaN for its norm.  d is at most FSDP_RMS_MAX_D; d = 0
+ * writes nothing, rstd included. */
 FSDP_API int fsdp_rms_norm_fp8(const void* x, fsdp_dtype x_dt, int64_t ldx, const void* residual,
                                fsdp_dtype h_dt, int64_t ldr, int64_t m, int64_t d, const void* weight,
                                fsdp_dtype w_dt, double eps, void* h, int64_t ldh, fsdp_dtype y_dt, void* y,

@@ -58,6 +58,8 @@ def fsdp_rms_norm_fp8(x, weight, residual=None, eps=1e-6, out=None, h=None, y=No
                  x of its dtype
     y            True, or a matrix: the normed rows as a tensor too (dtype of x for True)
 
+    Of no features rstd is NaN, the mean of nothing.
+
     No graph: where grad mode is on, an input that requires grad is refused, and so is one with a
     forward-mode tangent."""
     _no_tangents(x, weight, residual)
@@ -87,6 +89,9 @@ def fsdp_rms_norm_fp8(x, weight, residual=None, eps=1e-6, out=None, h=None, y=No
     else:
         y = None
     rstd = _vector(m, torch.float32, device, stream)
+    if d == 0:                                   # the mean of nothing; the call writes nothing
+        with _on(stream):
+            rstd.fill_(float("nan"))
     _issue("fsdp_rms_norm_fp8", device, stream, x.data_ptr(), dtype_code(x.dtype), ldx, res, cr, ldr, m, d,
            weight.data_ptr(), dtype_code(weight.dtype), float(eps), h.data_ptr() if res is not None else None, ldh, cy,
            py, ldy, *out._ptrs(), rstd.data_ptr())

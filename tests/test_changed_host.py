@@ -69,3 +69,10 @@ def test_a_graph_that_saved_the_residual_refuses_its_backward():
     ss.fsdp_rms_norm_fp8(torch.ones(3, 64), torch.ones(64), res.detach(), h=res.detach())
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+
+
+def test_rstd_of_no_features_is_not_what_memory_held(monkeypatch):
+    """Its mean is one of nothing: NaN."""
+    monkeypatch.setattr(rms, "_vector", lambda n, dtype, device, stream: torch.full((n,), 7.0, dtype=dtype))
+    o = ss.fsdp_rms_norm_fp8(torch.zeros(3, 0), torch.zeros(0))
+    assert o.rstd.shape == (3,) and o.rstd.isnan().all()

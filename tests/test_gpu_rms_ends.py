@@ -82,3 +82,14 @@ def test_products_over_the_largest_fp32(d):
         assert o.q.scales[0, 0] < 255 and torch.isinf(o.y[0, 3]) and o.q.scales[3, 0] == 255
         back = fp8_ref.values(o.q.codes.cpu().numpy(), o.q.scales.cpu().numpy(), d)
         assert abs(back[0, 3] - z[0, 3]) <= 2.0 ** -4 * z[0, 3]
+
+
+def test_rstd_of_no_features():
+    w = torch.empty(0, device="cuda")
+    for stream in (None, torch.cuda.Stream()):
+        torch.full((1000,), 5.0, device="cuda")                      # what the allocator would give next
+        o = ss.fsdp_rms_norm_fp8(torch.empty((1000, 0), device="cuda"), w, torch.empty((1000, 0), device="cuda"), stream=stream)
+        torch.cuda.synchronize()
+        assert o.rstd.isnan().all() and o.q.shape == (1000, 0) and o.h.shape == (1000, 0)
+        dx, dw = ss.fsdp_rms_norm_grads(o.h, o.h, w, o.rstd)
+        assert dx.shape == (1000, 0) and dw.shape == (0,)
