@@ -11,6 +11,7 @@ import ctypes
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version
 
 from . import _native as N
 from ._native import AdamWHP, OptimHP, Unit, View, check, i64_array, ptr_array
@@ -53,13 +54,13 @@ def _issue(name, device, stream, *args):
 
 
 def _changed(*given):
-    """Count a call's writes into the tensors that its caller gave for its results (what is no
-    tensor was not given), as torch's own in-place operations do: a graph that saved one of
+    """Count a call's writes into the tensors that its caller gave for its results (None, True and
+    False: none was given), as torch's own in-place operations do: a graph that saved one of
     them for its backward then refuses to run it on the new values.  Gathers do not count: the
     backward gathers the values again that the forward's views of the full buffer had."""
-    given = [t for t in given if isinstance(t, torch.Tensor)]
-    if given:
-        torch.autograd.graph.increment_version(given)
+    for t in given:
+        if t is not None and t is not True and t is not False:
+            increment_version(t)
 
 
 def _no_tangents(*inputs):
