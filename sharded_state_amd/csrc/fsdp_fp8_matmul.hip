@@ -31,9 +31,11 @@ constexpr int64_t kPart = 1 << 20;
 
 // The kinds of tiles.  Up to 16 rows of A the product is a read of B, and k_fp8_few has
 // more loads on their way than few tiles do (16 rows, us: 8192 x 8192 17.6 against 30.5 in
-// tiles, 5120 x 1280 4.4 and 6.8, 1000 x 1000 3.1 and 5.6, 28672 x 8192 49.4 and 50.6);
-// it holds the scales of 32 rows in LDS, hence kFewBlocks.  Else the largest tile that
-// gives at least 5/8 of the CUs one (us):
+// tiles, 5120 x 1280 4.4 and 6.8, 1000 x 1000 3.1 and 5.6);
+// it holds the scales of 32 rows in LDS, hence kFewBlocks.  Above 96 rows of B a CU the
+// tiles are taken, though k_fp8_few is ahead on both sides of that border (16 rows, us:
+// 24576 x 8192 42.0 against 48.0, 28672 x 8192 49.4 and 53.0, 50304 x 5120 58.6 and 75.0; one
+// row, 28672 x 8192 45.5 and 51.5).  Else the largest tile that gives at least 5/8 of the CUs one (us):
 //                       256     128, 2 stages   128, 4 stages   64 x 128   64
 //   4096 x 4096 x 4096  56.9    70.2            77.4            105.8      117.7
 //   6400 x 1600 x 1000  19.9    18.6            20.8            31.1       27.6

@@ -3,13 +3,17 @@
 //
 //   h = round(x + residual),  r = 1 / sqrt(sum(h^2) / d + eps),  y = (h * r) * w
 //
-// The memory bounds it: 5 bytes an element in bf16, 11 with a fp32 stream.  A row stays in
-// registers from its one read to its last use, and a workgroup that has more of them loads
-// the next before it sums this one.  The row's sum is held in 64 bits (a fp32 square
-// overflows above 1.8e19), and so is the product, which is rounded to codes once: through
-// fp32 one code in 2^20 would come out as its neighbour, at a gain of 1 to 8% of the time.
-// Measured: 8191 x 8192, bf16 on a fp32 stream, 142 us (5.2 TB/s); 8192 x 8192 bf16 91 us
-// (5.2); 1000 x 1600 fp16 5.6 us; one token of 1280 2.5 us.
+// The memory bounds it: 7 bytes an element in bf16 (3 without a residual), 11 on a fp32
+// stream.  A row stays in registers from its one read to its last use, and a workgroup that
+// has more of them loads the next before it sums this one.  That holds up to 16384 features.
+// Above, nothing is loaded ahead, and the 128 registers that 1024 lanes leave each of them do
+// not hold it all: 9 to 41 are spilled, 193 to 391 where rows are ragged (ragged rows with
+// fp32 in them spill up to 22 from 4096 features on).  The row's sum is held in 64 bits (a fp32 square overflows above 1.8e19),
+// and so is the product, which is rounded to codes once: through fp32 one code in 2^20
+// would come out as its neighbour, at a gain of 1 to 8% of the time.
+// Measured: 8191 x 8192, bf16 on a fp32 stream, 140 us (5.3 TB/s), with y too 167; 8192 x
+// 8192 bf16 89 us (5.3); 4096 x 12288 bf16 70 (5.0); 2048 x 32768 119 (4.0); ragged, 4096 x
+// 12287 90 (3.9) and 2048 x 20001 202 (1.4); 1000 x 1600 fp16 5.8; one token of 1280 2.6.
 #include "fsdp_rms_device.h"
 
 #pragma clang fp contract(off)

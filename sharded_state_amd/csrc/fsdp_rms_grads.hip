@@ -4,10 +4,14 @@
 //
 // The memory bounds it: 8 bytes an element in bf16.  A workgroup takes a row at a time, in
 // registers from its one read to its last use, with the next one's loads on their way; the
-// row's sum is held in 64 bits as the forward's is.
+// row's sum is held in 64 bits as the forward's is.  Above 8192 features nothing is loaded
+// ahead, and the 128 registers a lane do not hold it all: up to 38 are spilled, 73 to 289
+// where rows are ragged or longer than 16384 (ragged rows with fp32 in them spill up to 22
+// below 8192 too).  4096 x 12288 bf16 112 us (3.6 TB/s), with fp32 h 342 (2.1), 4096 x 12287
+// bf16 245 (1.7), 2048 x 20001 390 (0.8).
 // dw is added up by each workgroup over its rows in 32 bits, and the workgroups' sums by a
 // second launch in their order: no atomics, so the same call gives the same bits.  Measured:
-// 8192 x 8192 bf16 110 us (4.9 TB/s), 8191 x 8192 with fp32 h, dh and dx 184 us (5.1),
+// 8192 x 8192 bf16 108 us (5.0 TB/s), 8191 x 8192 with fp32 h, dh and dx 184 us (5.1),
 // 1000 x 1600 fp16 11.1 us, of which the second launch has a third.
 #include "fsdp_rms_device.h"
 
